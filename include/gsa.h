@@ -362,6 +362,72 @@ gsa_status gsa_forward_noalloc(const gsa_shape* shape, const gsa_bf16* q, const 
  * array's address cannot be looked up).  Allocates nothing. */
 gsa_status gsa_noalloc_check_device_error(void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A cache of views.  A reconstruction that runs view by view (a stream of
+ * frames, or new views placed in a scene that is already mapped) keeps the keys
+ * and values of the views it has seen, and every new view attends to that cache
+ * and to its own tokens.  prefix_attn is that attention for a whole batch of
+ * views that share one cache (the prefix: read once for all of them),
+ * key_weights keeps the account of how much attention each token received, and
+ * cache_evict shrinks the cache to the tokens with the largest account.
+ *
+ * Layouts: a token's heads lie side by side, 64 values each, and tokens lie a
+ * stride apart: q, out [n_q][H][64] and the keys and values
+ * [n_prefix][Hk][64], [n_own][Hk][64], where H is a multiple of Hk and query
+ * head h reads key head h / (H / Hk).  Strides count elements between tokens, 0
+ * standing for a dense layout; they are multiples of 8 that no token's heads
+ * reach over, so operands may be slices of a fused projection or of a larger
+ * cache.  Pointers are 16-byte aligned; one to a tensor without tokens
+ * (n_prefix or n_own = 0) is ignored and may be NULL.
+ * View b has the queries q_off[b] <= i < q_off[b + 1] and the own keys
+ * own_off[b] <= j < own_off[b + 1]; both are device int32 arrays of
+ * n_views + 1 offsets that do not decrease.  Rows that belong to no view (before
+ * q_off[0], or at and behind q_off[n_views] in a padded batch) are neither used
+ * nor written, whatever they hold.  Offsets that leave the buffers, and views
+ * longer than max_q or max_own, set the device-check bit: nothing outside the
+ * buffers is touched then, and the results are undefined.
+ * The values that a caller may not know in advance (offsets) are read on the
+ * device, so a captured call serves any batch that keeps to the sizes here.
+ * Infinite or NaN keys and values of one view never reach another view's rows.
+ */
+typedef struct {
+  int32_t n_views;     /* B >= 1 */
+  int32_t n_heads;     /* H in [1, 128] query heads */
+  int32_t n_kv_heads;  /* Hk >= 1, divides H */
+  int32_t head_dim;    /* only 64 is built */
+  int32_t n_q;         /* query tokens that q and out hold, >= 0 */
+  int32_t n_own;       /* own tokens that k_own and v_own hold, >= 0 */
+  int32_t n_prefix;    /* cached tokens, >= 0 */
+  int32_t max_q;       /* most queries of a view, in [0, n_q] */
+  int32_t max_own;     /* most own tokens of a view, in [0, n_own] */
+  int32_t causal;      /* 0: a query sees all tokens of its view; 1: the last query of a view
+                          sees all its own tokens, each query before it one token less */
+  float scale;         /* softmax scale; 0 means 1/sqrt(64) */
+  int32_t wait_limit_ns; /* as in gsa_shape */
+  int64_t q_stride, k_prefix_stride, v_prefix_stride, k_own_stride, v_own_stride, out_stride;
+} gsa_view_batch;
+
+/* Bytes of workspace prefix_attn and key_weights need for `batch` (the larger of
+ * the two; header included).  Host only. */
+gsa_status view_workspace_size(const gsa_view_batch* batch, size_t* bytes);
+
+/*
+ * Attention of a batch of views that share one prefix:
+ *   s[i][j] = scale * (q_i . k_j) over the prefix and the own keys that i sees,
+ *   out_i = sum_j softmax(s[i])_j v_j  [n_q][H][64] bf16,
+ *   lse [n_q][H] fp32 = log sum_j exp s[i][j]  (may be NULL).
+ * A query that sees no key gets zeros and an lse of -infinity.  `out` must not
+ * overlap any input.  Views of a few tokens, single ones among them, are packed
+ * into shared tiles, and long key ranges are split over the GPU and merged in
+ * the workspace (in a fixed order: equal calls give equal bits).
+ * With `causal`, a NaN or infinite own value may reach queries of its own view
+ * that do not see it.
+ */
+gsa_status prefix_attn(const gsa_view_batch* batch, const gsa_bf16* q, const gsa_bf16* k_prefix,
+                       const gsa_bf16* v_prefix, const gsa_bf16* k_own, const gsa_bf16* v_own,
+                       const int32_t* q_off, const int32_t* own_off, gsa_bf16* out, float* lse, void* ws,
+                       size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read the device error word in `ws`, clear it, and
  * return GSA_OK, GSA_ERR_TIMEOUT or GSA_ERR_DEVICE_CHECK.  For diagnosis, the
  * header's words 1 and 2 record the first in-kernel wait that ran out (its

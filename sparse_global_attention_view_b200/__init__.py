@@ -32,3 +32,9 @@ from .api import (  # noqa: F401
     workspace_size,
     workspace_view,
 )
+from .views import (  # noqa: F401
+    ViewBatch,
+    new_view_workspace,
+    prefix_attn,
+    view_workspace_size,
+)

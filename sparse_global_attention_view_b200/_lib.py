@@ -70,9 +70,18 @@ class GsaWsOffsets(ctypes.Structure):
                                       "total")] + [("n_split", c_i32), ("best", c_size), ("order", c_size)]
 
 
+class GsaViewBatch(ctypes.Structure):
+    _fields_ = [(n, c_i32) for n in ("n_views", "n_heads", "n_kv_heads", "head_dim", "n_q", "n_own",
+                                      "n_prefix", "max_q", "max_own", "causal")] + [
+        ("scale", c_f32), ("wait_limit_ns", c_i32)] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "k_prefix_stride", "v_prefix_stride", "k_own_stride",
+                                      "v_own_stride", "out_stride")]
+
+
 FORWARD_STEPS = ("pool", "compressed_attn", "block_scores", "topk_merge", "kept_attn", "selected_gate")
 
 P_SHAPE = ctypes.POINTER(GsaShape)
+P_VIEWS = ctypes.POINTER(GsaViewBatch)
 
 # name -> argument types (all return gsa_status, an int, except gsa_status_string)
 SIGNATURES = {
@@ -95,6 +104,8 @@ SIGNATURES = {
     "gsa_workspace_offsets": [P_SHAPE, ctypes.POINTER(GsaWsOffsets)],
     "gsa_forward_noalloc": [P_SHAPE] + [c_vp] * 6,
     "gsa_noalloc_check_device_error": [c_vp],
+    "view_workspace_size": [P_VIEWS, ctypes.POINTER(c_size)],
+    "prefix_attn": [P_VIEWS] + [c_vp] * 10 + [c_size, c_vp],
     "gsa_check_device_error": [c_vp, c_vp],
     "gsa_selftest_exp2": [c_vp, c_vp, ctypes.c_int64, c_vp],
     "gsa_status_string": [c_i32],

@@ -1,0 +1,779 @@
+// Attention of a batch of views that share one prefix (a cache of the views
+// seen so far): softmax over the prefix and the view's own keys.
+//
+// For query i of view b (rows packed one behind the other, views ragged):
+//   s_ij = scale q_i . k_j over the prefix keys and the view's own keys,
+//   out_i = sum_j exp(s_ij - lse_i) v_j,  lse_i = log sum_j exp s_ij.
+// The softmax is associative over key ranges, so ranges are taken by different
+// CTAs where there are few rows, and (out, lse) pairs are merged afterwards.
+//
+// view_attn_kernel (tcgen05 / TMEM / TMA): one CTA = up to two 128-row query
+// tiles of one key head.  A row is a (token, query head of the group) pair, so
+// the G query heads that share a key head share its K/V tiles.  12 warps:
+//   warp 0      TMA producer: the Q tiles once, then a 6-stage ring of 128-key K/V
+//               tiles; zeroes the value rows behind a view's last key;
+//   warps 1, 3  MMA issuers, one for each tile: S = Q K^T into TMEM, O += P V with P from TMEM;
+//   warp 2      TMEM allocation;
+//   warps 4-11  softmax, one warpgroup a tile, one thread a row.
+// The softmax takes a score tile into registers and hands S back at once, and P
+// has columns of its own (S 2 x 128, O 2 x 64, P 2 x 64 of the 512), so the next
+// Q K^T runs while the exponentials of the present tile are taken; a warp never
+// waits for a product in the steady state.  Bound by the exponentials and the
+// instructions around them (two per 128 flops at a head width of 64).
+// With at most 128 rows the two slots take alternate key tiles of the same
+// rows instead; their results count as separate partial results.
+//
+// view_own_kernel: views of few rows.  Their own keys are read by CUDA cores
+// (eight lanes a key, plain 16-byte loads: nothing is read that no query sees),
+// and the partial results against the prefix are merged in the same pass.
+// merge_kernel: partial results only.
+//
+// Every sum, maximum and partial result is fp32; P is rounded to bf16 for the
+// product with V (a relative 2^-9 each, independent between keys), and the
+// denominator sums the unrounded weights.
+#include <math.h>
+#include <math_constants.h>
+
+#include "exp2_poly.cuh"
+#include "views.h"
+
+namespace gsa {
+namespace {
+
+using namespace tc;
+
+constexpr int kPolyOf8 = 2;  // pairs of exponentials in eight on the FMA pipe
+constexpr int TK = 128;      // keys per key tile
+constexpr int ST = 6;        // K/V ring stages
+constexpr int kThreads = 384;
+constexpr uint32_t kTile = 128 * 128;  // bytes of one [128][64] bf16 tile
+
+constexpr uint32_t OFF_Q = 0;
+constexpr uint32_t OFF_K = OFF_Q + 2 * kTile;
+constexpr uint32_t OFF_V = OFF_K + ST * kTile;
+constexpr uint32_t OFF_BAR = OFF_V + ST * kTile;
+constexpr uint32_t OFF_MISC = OFF_BAR + 256;
+constexpr uint32_t kSmemBytes = OFF_MISC + 64 + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+constexpr int B_Q = 0, B_KF = 1, B_VF = B_KF + ST, B_KVE = B_VF + ST, B_SF = B_KVE + ST, B_SE = B_SF + 2,
+              B_PF = B_SE + 2, B_PE = B_PF + 2, B_VZ = B_PE + 2, B_DRAIN = B_VZ + 1, B_COUNT = B_DRAIN + 2;
+static_assert(B_COUNT * 8 <= 256, "barrier area");
+
+constexpr uint32_t kCols = 512, COL_O = 256, COL_P = 384;  // TMEM: S_t at 128 t, O_t, P_t at 64 t behind
+constexpr int kLaunchRegs = 168, kRegsLow = 72, kRegsHigh = 216;
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kLaunchRegs, "register split");
+
+struct ViewAttnArgs {
+  ViewDims d;
+  int rows_tok;   // tokens per row tile: 128 / G
+  int aligned, do_prefix, do_own, pair, check_views;
+  int n_split, units_per_view;
+  bf16* out;      // written directly when part_o is null
+  float* lse;     // nullable
+  float* part_o;  // [parts][n_q][H][64], normalised
+  float* part_lse;  // [parts][n_q][H], log2 units
+  int part0;
+  unsigned* err;
+};
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err,
+                                          long long limit) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, limit));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    view_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tkp,
+                     const __grid_constant__ CUtensorMap tvp, const __grid_constant__ CUtensorMap tko,
+                     const __grid_constant__ CUtensorMap tvo, const ViewAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t tc_smem_raw[];
+  const uint32_t raw = smem_u32(tc_smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* sp = tc_smem_raw + (sb - raw);
+  const uint32_t sQ = sb + OFF_Q, sK = sb + OFF_K, sV = sb + OFF_V;
+  auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + OFF_MISC + 4);
+
+  const ViewDims& d = a.d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hk = blockIdx.y;
+  const int unit = blockIdx.x / a.n_split, split = blockIdx.x - unit * a.n_split;
+  const int MT = a.rows_tok, unit_tok = a.pair ? MT : 2 * MT;
+
+  // this CTA's rows [tok0, tok_end) and keys; uniform over the CTA
+  long long tok0;
+  int tok_lo, tok_end, q0 = 0, nq = 0, k0 = 0, nk = 0;
+  if (a.aligned) {
+    const int b = unit / a.units_per_view, c = unit - b * a.units_per_view;
+    ViewRange r;
+    if (!view_range(d, b, &r, a.err)) return;
+    tok0 = (long long)r.q0 + (long long)c * unit_tok;
+    if (tok0 >= r.q1) return;
+    tok_lo = q0 = r.q0;
+    tok_end = r.q1;
+    nq = r.q1 - r.q0;
+    k0 = r.k0;
+    nk = a.do_own ? r.k1 - r.k0 : 0;
+  } else {
+    tok0 = (long long)unit * unit_tok;
+    tok_lo = max(d.q_off[0], 0);
+    tok_end = min(d.q_off[d.B], d.n_q);
+    if (tok0 >= tok_end || tok0 + unit_tok <= tok_lo) return;
+  }
+  const int last_row = (int)min(tok0 + unit_tok, (long long)tok_end) - 1;
+  // own keys seen by at least one of the rows
+  int nk_seen = nk;
+  if (d.causal) nk_seen = max(0, min(nk, last_row - q0 + nk - nq + 1));
+  const int np = a.do_prefix ? (d.n_prefix + TK - 1) / TK : 0;
+  const int nt_all = np + (nk_seen + TK - 1) / TK;
+  const int j0 = (int)((long long)nt_all * split / a.n_split);
+  const int nt = (int)((long long)nt_all * (split + 1) / a.n_split) - j0;
+  // steps of slot t: its i-th one is key tile j0 + i, or j0 + 2 i + t
+  const int active = a.pair ? 2 : (tok0 + MT < tok_end ? 2 : 1);
+  auto steps = [&](int t) -> int { return t >= active ? 0 : (a.pair ? (nt + 1 - t) / 2 : nt); };
+  // the value rows behind the view's last seen key hold other tokens: zeroed
+  const bool zero_tail = nt > 0 && j0 + nt == nt_all && nt_all > np && (nk_seen % TK) != 0;
+
+  if (tid == 0) {
+    mbar_init(bar(B_Q), 1);
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(bar(B_KF + s), 1);
+      mbar_init(bar(B_VF + s), 1);
+      mbar_init(bar(B_KVE + s), a.pair ? 1 : active);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(B_SF + t), 1);
+      mbar_init(bar(B_SE + t), 4);
+      mbar_init(bar(B_PF + t), 4);
+      mbar_init(bar(B_PE + t), 1);
+      mbar_init(bar(B_DRAIN + t), 1);
+    }
+    mbar_init(bar(B_VZ), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(tmem_slot), kCols);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tbase = *tmem_slot;
+  const long long limit = d.wait_cycles;
+
+  if (warp < 4) regs_dec<kRegsLow>();
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (lane == 0 && nt > 0) {
+      const int q_tiles = a.pair ? 1 : active;
+      mbar_expect_tx(bar(B_Q), (uint32_t)(q_tiles * MT * d.G) * 128u);
+      for (int t = 0; t < q_tiles; ++t) tma_load_3d(sQ + t * kTile, &tq, bar(B_Q), 0, hk * d.G, (int)(tok0 + t * MT));
+      int issued = 0;
+      for (int i = 0; i < nt; ++i) {
+        const int s = i % ST;
+        if (i >= ST && !mbar_wait(bar(B_KVE + s), ((i / ST) - 1) & 1, abort_flag, a.err, limit)) break;
+        const int j = j0 + i;
+        const bool pre = j < np;
+        const int row = pre ? j * TK : k0 + (j - np) * TK;
+        mbar_expect_tx(bar(B_KF + s), kTile);
+        tma_load_3d(sK + s * kTile, pre ? &tkp : &tko, bar(B_KF + s), 0, hk, row);
+        mbar_expect_tx(bar(B_VF + s), kTile);
+        tma_load_3d(sV + s * kTile, pre ? &tvp : &tvo, bar(B_VF + s), 0, hk, row);
+        issued = i + 1;
+      }
+      // this CTA's own copies land before its shared memory goes away, whatever
+      // becomes of the other warps
+      volatile int never = 0;
+      mbar_wait(bar(B_Q), 0, &never, a.err);
+      for (int i = issued - 1; i >= 0 && i >= issued - ST; --i) {
+        mbar_wait(bar(B_KF + i % ST), (i / ST) & 1, &never, a.err);
+        mbar_wait(bar(B_VF + i % ST), (i / ST) & 1, &never, a.err);
+      }
+    }
+    __syncwarp();
+    if (zero_tail && !*abort_flag) {
+      // value rows of other tokens: their weights are 0, but 0 x infinity or NaN
+      // is not.  The last copy has been issued, so its phase is the one waited for
+      const int i = nt - 1, s = i % ST;
+      if (warp_wait(bar(B_VF + s), (i / ST) & 1, abort_flag, a.err, limit)) {
+        uint8_t* v = sp + OFF_V + s * kTile;
+        for (uint32_t o = (uint32_t)(nk_seen % TK) * 128u + lane * 16u; o < kTile; o += 512u)
+          *reinterpret_cast<uint4*>(v + o) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_VZ));
+      }
+    }
+  } else if (warp == 1 || warp == 3) {
+    // ---------------- MMA issuer of slot t ----------------
+    const int t = warp >> 1;
+    const int n = steps(t);
+    if (lane == 0 && n > 0) {
+      const uint32_t id_qk = idesc(128, 128, kFmtBF16, 0, 0);
+      const uint32_t id_pv = idesc(128, 64, kFmtBF16, 0, 1);
+      const uint32_t q_tile = sQ + (a.pair ? 0 : t) * kTile;
+      auto at = [&](int i) -> int { return a.pair ? 2 * i + t : i; };  // ring index of step i
+      auto issue_s = [&](int i) {
+        const uint32_t k_tile = sK + (at(i) % ST) * kTile;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_bf16_ss(tbase + t * 128, sdesc_k(q_tile + kk * 32), sdesc_k(k_tile + kk * 32), id_qk, kk > 0);
+        mma_commit(bar(B_SF + t));
+      };
+      auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, a.err, limit); };
+      auto k_full = [&](int i) { return wait(B_KF + at(i) % ST, (at(i) / ST) & 1); };
+      bool ok = wait(B_Q, 0) && k_full(0);
+      if (ok) {
+        fence_after_sync();
+        issue_s(0);
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        if (i + 1 < n) {
+          ok = k_full(i + 1) && wait(B_SE + t, i & 1);
+          if (!ok) break;
+          fence_after_sync();
+          issue_s(i + 1);
+        }
+        const int s = at(i) % ST;
+        ok = wait(B_VF + s, (at(i) / ST) & 1);
+        if (ok && zero_tail && at(i) == nt - 1) ok = wait(B_VZ, 0);
+        ok = ok && wait(B_PF + t, i & 1);
+        if (!ok) break;
+        fence_after_sync();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ts(tbase + COL_O + t * 64, tbase + COL_P + t * 64 + kk * 8, sdesc_mn(sV + s * kTile + kk * 2048),
+                      id_pv, (i > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(bar(B_PE + t));
+        mma_commit(bar(B_KVE + s));
+      }
+      if (!ok) {
+        // wait for the products already issued before TMEM is released
+        volatile int never = 0;
+        mma_commit(bar(B_DRAIN + t));
+        mbar_wait(bar(B_DRAIN + t), 0, &never, a.err);
+      }
+    }
+  } else if (warp == 2) {
+    // a launch that reads no own keys still reports offsets that promise some
+    if (!a.aligned && a.check_views && blockIdx.x == 0 && blockIdx.y == 0) {
+      ViewRange r;
+      for (int b = lane; b < d.B; b += 32) view_range(d, b, &r, a.err);
+    }
+  } else {
+    regs_inc<kRegsHigh>();
+    // ---------------- softmax, one thread a row ----------------
+    const int t = (warp - 4) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const int tl = row / d.G, g = row - tl * d.G;
+    const long long tok = tok0 + (a.pair ? 0 : t * MT) + tl;
+    const bool valid = t < active && tl < MT && tok >= tok_lo && tok < tok_end;
+    // own keys [0, own_end) of the view are seen by this row
+    int own_end = nk;
+    if (d.causal && valid) own_end = max(0, min(nk, (int)(tok - q0) + nk - nq + 1));
+    const bool work = __any_sync(0xffffffffu, valid);
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tbase + lane_off + t * 128;
+    const uint32_t o_addr = tbase + lane_off + COL_O + t * 64;
+    const uint32_t p_addr = tbase + lane_off + COL_P + t * 64;
+    const float c2 = d.c2;
+    const int n = steps(t);
+    float m_used = -CUDART_INF_F, l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      ok = warp_wait(bar(B_SF + t), i & 1, abort_flag, a.err, limit);
+      if (!ok) break;
+      fence_after_sync();
+      if (!work) {
+        // no rows: only the barriers, in step with the other warps
+        if (lane == 0) mbar_arrive(bar(B_SE + t));
+        if (i > 0) ok = warp_wait(bar(B_PE + t), (i - 1) & 1, abort_flag, a.err, limit);
+        if (!ok) break;
+        fence_before_sync();
+        if (lane == 0) mbar_arrive(bar(B_PF + t));
+        continue;
+      }
+      uint32_t sv[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, sv[c]);
+      tmem_wait_ld();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_SE + t));
+      const int j = j0 + (a.pair ? 2 * i + t : i);
+      const int end = j < np ? d.n_prefix - j * TK : own_end - (j - np) * TK;
+      if (end < TK) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            if (32 * c + u >= end) sv[c][u] = __float_as_uint(-CUDART_INF_F);
+      }
+      // eight independent chains: a thread owns a whole row
+      auto sval = [&](int k) -> float { return __uint_as_float(sv[k >> 5][k & 31]); };
+      float mq[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) mq[u] = max_nan(sval(u), sval(u + 8));
+#pragma unroll
+      for (int k = 16; k < 128; k += 16)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mq[u] = max3_nan(mq[u], sval(k + u), sval(k + 8 + u));
+      const float mx = max3_nan(max3_nan(mq[0], mq[1], mq[2]), max3_nan(mq[3], mq[4], mq[5]), max_nan(mq[6], mq[7]));
+      float mxs = mx * c2;
+      if (mxs == CUDART_INF_F) mxs = CUDART_NAN_F;  // infinity - infinity
+      // the maximum in use is raised only when a score exceeds it by 2^8; a NaN
+      // score makes it NaN, and with it the row
+      const bool need = !(mxs <= m_used + 8.f);
+      if (__any_sync(0xffffffffu, need)) {
+        const float corr = need ? exp2f(m_used - mxs) : 1.f;
+        if (i > 0) {
+          ok = warp_wait(bar(B_PE + t), (i - 1) & 1, abort_flag, a.err, limit);
+          if (!ok) break;
+          fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t ov[16];
+            tmem_ld16(o_addr + 16 * c, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 16; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * corr);
+            tmem_st16(o_addr + 16 * c, ov);
+          }
+        }
+        if (need) {
+          l *= corr;
+          m_used = mxs;
+        }
+      }
+      // a row that has seen no key yet keeps finite arithmetic: weights 2^-inf = 0
+      const float shift = m_used == -CUDART_INF_F ? 0.f : -m_used;
+      const uint64_t c2p = f2_pack(c2, c2), nmp = f2_pack(shift, shift);
+      uint64_t ps2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const uint64_t x2 =
+              f2_fma(f2_pack(__uint_as_float(sv[c][2 * u]), __uint_as_float(sv[c][2 * u + 1])), c2p, nmp);
+          uint64_t p2;
+          if ((u & 7) >= 8 - kPolyOf8) {
+            p2 = exp2_poly2(x2);
+          } else {
+            float x0, x1;
+            f2_unpack(x2, x0, x1);
+            p2 = f2_pack(exp2_mufu(x0), exp2_mufu(x1));
+          }
+          ps2[u & 3] = f2_add(ps2[u & 3], p2);
+          float p0, p1;
+          f2_unpack(p2, p0, p1);
+          pk[u] = pack_bf16x2(p0, p1);
+        }
+        // P of the step before has to be read before it is written over
+        if (c == 0 && i > 0) {
+          ok = warp_wait(bar(B_PE + t), (i - 1) & 1, abort_flag, a.err, limit);
+          if (!ok) break;
+          fence_after_sync();
+        }
+        tmem_st16(p_addr + 16 * c, pk);
+      }
+      if (!ok) break;
+      tmem_wait_st();
+      {
+        const uint64_t s01 = f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3]));
+        float lo, hi;
+        f2_unpack(s01, lo, hi);
+        l += lo + hi;
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_PF + t));
+    }
+    if (ok && n > 0) ok = warp_wait(bar(B_PE + t), (n - 1) & 1, abort_flag, a.err, limit);
+    if (ok && work) {
+      fence_after_sync();
+      // no key seen: zeros and a log sum of -infinity (a NaN score left l NaN)
+      const bool empty = m_used == -CUDART_INF_F && !(l != l);
+      const float inv = empty ? 0.f : 1.f / l;
+      const float lse2 = empty ? -CUDART_INF_F : m_used + log2f(l);
+      const int h = hk * d.G + g;
+      const long long rh = tok * d.H + h;
+      const long long part = a.part0 + (a.pair ? 2 * split + t : split);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t ov[16];
+        if (n > 0) {
+          tmem_ld16(o_addr + 16 * c, ov);
+          tmem_wait_ld();
+        }
+        if (!valid) continue;
+        float o[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) o[u] = empty ? 0.f : __uint_as_float(ov[u]) * inv;
+        if (a.part_o) {
+          if (empty) continue;  // the merge skips it by its log sum
+          float4* dst = reinterpret_cast<float4*>(a.part_o + ((part * d.n_q * d.H + rh) * 64 + 16 * c));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        } else {
+          uint32_t w[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) w[u] = pack_bf16x2(o[2 * u], o[2 * u + 1]);
+          uint4* dst = reinterpret_cast<uint4*>(a.out + tok * d.o_stride + h * 64 + 16 * c);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      if (valid) {
+        if (a.part_o)
+          a.part_lse[part * d.n_q * d.H + rh] = lse2;
+        else if (a.lse)
+          a.lse[rh] = lse2 * 0.6931471805599453f;
+      }
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 2) {
+    fence_after_sync();
+    tmem_dealloc(tbase, kCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// merging partial results
+
+// Merges (o, lse2) pairs; o normalised.  A pair of lse2 = -infinity holds no key.
+struct Merge {
+  float m;  // largest lse2 so far, NaN ones aside
+  float l;  // sum of 2^(lse2 - m)
+  __device__ __forceinline__ Merge() : m(-INFINITY), l(0.f) {}
+  // factor of the sums so far, and weight of the new pair
+  __device__ __forceinline__ bool add(float lse2, float* keep, float* w) {
+    if (lse2 == -CUDART_INF_F) return false;
+    const float mn = fmaxf(m, lse2);
+    *keep = m == -CUDART_INF_F ? 0.f : exp2f(m - mn);
+    *w = exp2f(lse2 - mn);
+    l = l * *keep + *w;
+    m = mn;
+    return true;
+  }
+  __device__ __forceinline__ float lse() const {
+    return l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+  }
+  __device__ __forceinline__ float inv() const { return l == 0.f ? 0.f : 1.f / l; }
+};
+
+// Eight lanes a (token, head); every lane eight of the 64 values.
+__global__ void __launch_bounds__(256) merge_kernel(const ViewDims d, int parts, const float* __restrict__ part_o,
+                                                    const float* __restrict__ part_lse, bf16* __restrict__ out,
+                                                    float* __restrict__ lse) {
+  const long long rh = ((long long)blockIdx.x * 256 + threadIdx.x) >> 3;
+  const int e = (threadIdx.x & 7) * 8;
+  const long long n = (long long)d.n_q * d.H;
+  if (rh >= n) return;
+  const int tok = (int)(rh / d.H), h = (int)(rh - (long long)tok * d.H);
+  if (tok < d.q_off[0] || tok >= d.q_off[d.B]) return;
+  Merge mg;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < parts; ++p) {
+    float keep, w;
+    if (!mg.add(part_lse[p * n + rh], &keep, &w)) continue;
+    const float4* src = reinterpret_cast<const float4*>(part_o + (p * n + rh) * 64 + e);
+    const float4 x = src[0], y = src[1];
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int u = 0; u < 8; ++u) acc[u] = acc[u] * keep + v[u] * w;
+  }
+  const float inv = mg.inv();
+  uint32_t w[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) w[u] = pack_bf16x2(acc[2 * u] * inv, acc[2 * u + 1] * inv);
+  *reinterpret_cast<uint4*>(out + tok * d.o_stride + h * 64 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (lse && e == 0) lse[rh] = mg.lse();
+}
+
+// ---------------------------------------------------------------------------
+// own keys of views with few rows, merged with the prefix's partial results
+
+constexpr int OWN_R = 4;       // rows in registers at a time
+constexpr int OWN_WARPS = 4;
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// One block = one view and key head.  Eight lanes hold a key's 64 values; the
+// block's 16 groups of eight take the keys in turn, each with a softmax of its
+// own, merged at the end.
+__global__ void __launch_bounds__(32 * OWN_WARPS)
+    view_own_kernel(const ViewDims d, const bf16* __restrict__ q, const bf16* __restrict__ k,
+                    const bf16* __restrict__ v, int parts, const float* __restrict__ part_o,
+                    const float* __restrict__ part_lse, bf16* __restrict__ out, float* __restrict__ lse, unsigned* err) {
+  const int b = blockIdx.x, hk = blockIdx.y;
+  ViewRange r;
+  if (!view_range(d, b, &r, err)) return;
+  __shared__ float s_m[OWN_WARPS][OWN_R], s_l[OWN_WARPS][OWN_R], s_o[OWN_WARPS][OWN_R][64];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = (lane & 7) * 8, grp = tid >> 3;
+  const int nq = r.q1 - r.q0, nk = r.k1 - r.k0, rows = nq * d.G;
+  const long long n = (long long)d.n_q * d.H;
+  for (int r0 = 0; r0 < rows; r0 += OWN_R) {
+    float qf[OWN_R][8], o[OWN_R][8], m[OWN_R], l[OWN_R];
+    int end[OWN_R];
+    int end_max = 0;
+#pragma unroll
+    for (int i = 0; i < OWN_R; ++i) {
+      const int row = min(r0 + i, rows - 1), tl = row / d.G, h = hk * d.G + row - tl * d.G;
+      const uint4 u = *reinterpret_cast<const uint4*>(q + (r.q0 + tl) * d.q_stride + h * 64 + e);
+      unpack8(u, qf[i]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        qf[i][c] *= d.c2;
+        o[i][c] = 0.f;
+      }
+      m[i] = -CUDART_INF_F;
+      l[i] = 0.f;
+      end[i] = d.causal ? max(0, min(nk, tl + nk - nq + 1)) : nk;
+      end_max = max(end_max, end[i]);
+    }
+    for (int j0 = 0; j0 < end_max; j0 += 4 * OWN_WARPS) {
+      const int j = j0 + grp;
+      const bool live = j < end_max;
+      float kf[8], vf[8];
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 ku = live ? *reinterpret_cast<const uint4*>(k + (r.k0 + j) * d.ko_stride + hk * 64 + e) : zero;
+      const uint4 vu = live ? *reinterpret_cast<const uint4*>(v + (r.k0 + j) * d.vo_stride + hk * 64 + e) : zero;
+      unpack8(ku, kf);
+      unpack8(vu, vf);
+#pragma unroll
+      for (int i = 0; i < OWN_R; ++i) {
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s = fmaf(qf[i][c], kf[c], s);
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        if (j < end[i]) {
+          // exp2f(-infinity - -infinity) would be NaN for scores of -infinity
+          const float mn = fmaxf(m[i], s);
+          const float corr = m[i] == mn ? 1.f : exp2f(m[i] - mn);
+          const float p = s == -CUDART_INF_F ? 0.f : exp2f(s - mn);
+          l[i] = l[i] * corr + p;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) o[i][c] = fmaf(p, vf[c], o[i][c] * corr);
+          m[i] = mn;
+        }
+      }
+    }
+    // the four groups of the warp, then the warps
+#pragma unroll
+    for (int i = 0; i < OWN_R; ++i) {
+#pragma unroll
+      for (int x = 8; x <= 16; x <<= 1) {
+        const float mo = __shfl_xor_sync(0xffffffffu, m[i], x), lo = __shfl_xor_sync(0xffffffffu, l[i], x);
+        const float mn = fmaxf(m[i], mo);
+        const float ca = m[i] == mn ? 1.f : exp2f(m[i] - mn), cb = mo == mn ? 1.f : exp2f(mo - mn);
+        l[i] = l[i] * ca + lo * cb;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float oo = __shfl_xor_sync(0xffffffffu, o[i][c], x);
+          o[i][c] = o[i][c] * ca + oo * cb;
+        }
+        m[i] = mn;
+      }
+      if (lane < 8) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s_o[warp][i][e + c] = o[i][c];
+        if (lane == 0) {
+          s_m[warp][i] = m[i];
+          s_l[warp][i] = l[i];
+        }
+      }
+    }
+    __syncthreads();
+    // warp i: row i; lanes 0-7 carry it on with the prefix's results
+    if (lane < 8 && warp < OWN_R && r0 + warp < rows) {
+      const int row = r0 + warp, tl = row / d.G, h = hk * d.G + row - tl * d.G, tok = r.q0 + tl;
+      Merge mg;
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < OWN_WARPS; ++w) {
+        const float lw = s_l[w][warp], mw = s_m[w][warp];
+        if (lw == 0.f) continue;
+        float keep, wt;
+        if (!mg.add(mw + log2f(lw), &keep, &wt)) continue;
+        const float f = wt / lw;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = acc[c] * keep + s_o[w][warp][e + c] * f;
+      }
+      const long long rh = (long long)tok * d.H + h;
+      for (int p = 0; p < parts; ++p) {
+        float keep, wt;
+        if (!mg.add(part_lse[p * n + rh], &keep, &wt)) continue;
+        const float4* src = reinterpret_cast<const float4*>(part_o + (p * n + rh) * 64 + e);
+        const float4 x = src[0], y = src[1];
+        const float pv[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = acc[c] * keep + pv[c] * wt;
+      }
+      const float inv = mg.inv();
+      uint32_t w[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) w[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+      *reinterpret_cast<uint4*>(out + tok * d.o_stride + h * 64 + e) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (lse && e == 0) lse[rh] = mg.lse();
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+
+cudaError_t prepare_kernel() {
+  cudaError_t e = cudaFuncSetAttribute(view_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, view_attn_kernel);
+  if (e != cudaSuccess) return e;
+  // the register split waits forever on another launch allocation
+  return fa.numRegs == kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+// Key splits for `units` CTAs of `tiles` key tiles each on 148 SMs.  Costs are
+// counted in key tiles: a CTA's start and end take about as long as `fixed` of
+// them, and a merged result costs `merge` more for each split.
+int choose_split(long long units, int tiles, int most, double fixed, double merge) {
+  int best = 1;
+  double best_cost = 0;
+  for (int s = 1; s <= most && s <= tiles; ++s) {
+    const double waves = (double)((units * s + 147) / 148);
+    const double cost = waves * (ceil_div(tiles, s) + fixed) + (s > 1 ? merge * s : 0.0);
+    if (s == 1 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+ViewPlan view_plan(const ViewDims& d) {
+  ViewPlan p = {};
+  p.split_packed = p.split_aligned = 1;
+  const int MT = 128 / d.G;
+  const int np = ceil_div(d.n_prefix, TK), no = ceil_div(d.max_own, TK);
+  const bool has_own = d.n_own > 0 && d.max_own > 0;
+  const bool short_views = (long long)d.max_q * d.G <= 16 && d.max_own <= 4096;
+  if (!has_own || short_views || (d.n_prefix > 0 && d.B > 1 && d.n_q < 2LL * MT * d.B)) {
+    p.packed = d.n_prefix > 0;
+    p.small_own = has_own && short_views;
+    p.aligned = p.aligned_own = has_own && !short_views;
+  } else {
+    p.aligned = p.aligned_own = 1;
+    p.aligned_prefix = d.n_prefix > 0;
+  }
+  // partial results of one launch of a kind: their bytes against a key tile's time
+  const double merge = 1.0 + (double)d.n_q * d.H * 64 * 8 / 3.0e6;
+  if (p.packed) {
+    p.pair_packed = d.n_q <= MT;
+    const long long units = (long long)ceil_div(d.n_q, p.pair_packed ? MT : 2 * MT) * d.Hk;
+    p.split_packed = choose_split(units, np, 64, 4.0, merge);
+    p.parts += p.split_packed * (p.pair_packed ? 2 : 1);
+  }
+  if (p.aligned) {
+    p.pair_aligned = d.max_q <= MT;
+    const int unit_tok = p.pair_aligned ? MT : 2 * MT;
+    long long units = (long long)d.B * ceil_div(d.max_q, unit_tok);
+    const long long bound = d.n_q / unit_tok + d.B;  // rows there are, and a ragged end a view
+    if (units > bound) units = bound;
+    p.split_aligned = choose_split(units * d.Hk, (p.aligned_prefix ? np : 0) + no, 64, 4.0, merge);
+    p.parts += p.split_aligned * (p.pair_aligned ? 2 : 1);
+  }
+  // one part that nothing else joins is the result
+  if (p.parts == 1 && !p.small_own) p.parts = 0;
+  return p;
+}
+
+cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16* q, const bf16* kp, const bf16* vp,
+                               const bf16* ko, const bf16* vo, bf16* out, float* lse, float* part_o, float* part_lse,
+                               unsigned* err, cudaStream_t st) {
+  if (d.n_q <= 0) return cudaSuccess;
+  const int MT = 128 / d.G;
+  if (p.packed || p.aligned) {
+    cudaError_t e = prepare_kernel();
+    if (e != cudaSuccess) return e;
+    CUtensorMap mq, mkp, mvp, mko, mvo;
+    auto map = [&](CUtensorMap* m, const bf16* base, int heads, int rows, long long stride, int b1, int b2) {
+      return make_tmap_3d(m, false, base, 64, (unsigned long long)heads, (unsigned long long)rows, 128,
+                          (unsigned long long)stride * 2, 64, (unsigned)b1, (unsigned)b2);
+    };
+    bool ok = map(&mq, q, d.H, d.n_q, d.q_stride, d.G, MT);
+    if (d.n_prefix > 0)
+      ok = ok && map(&mkp, kp, d.Hk, d.n_prefix, d.kp_stride, 1, TK) && map(&mvp, vp, d.Hk, d.n_prefix, d.vp_stride, 1, TK);
+    if (d.n_own > 0)
+      ok = ok && map(&mko, ko, d.Hk, d.n_own, d.ko_stride, 1, TK) && map(&mvo, vo, d.Hk, d.n_own, d.vo_stride, 1, TK);
+    if (!ok) return cudaErrorInvalidValue;
+    // a map that no tile uses still has to be one
+    if (d.n_prefix <= 0) mkp = mvp = mq;
+    if (d.n_own <= 0) mko = mvo = mq;
+    ViewAttnArgs a = {};
+    a.d = d;
+    a.rows_tok = MT;
+    a.out = out;
+    a.lse = lse;
+    a.part_o = p.parts ? part_o : nullptr;
+    a.part_lse = part_lse;
+    a.err = err;
+    if (p.packed) {
+      a.aligned = 0;
+      a.do_prefix = 1;
+      a.do_own = 0;
+      a.check_views = !p.aligned && !p.small_own;
+      a.pair = p.pair_packed;
+      a.n_split = p.split_packed;
+      a.units_per_view = 0;
+      a.part0 = 0;
+      const dim3 grid((unsigned)(ceil_div(d.n_q, a.pair ? MT : 2 * MT) * a.n_split), (unsigned)d.Hk);
+      view_attn_kernel<<<grid, kThreads, kSmemBytes, st>>>(mq, mkp, mvp, mko, mvo, a);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      a.part0 = p.split_packed * (p.pair_packed ? 2 : 1);
+    }
+    if (p.aligned) {
+      a.aligned = 1;
+      a.do_prefix = p.aligned_prefix;
+      a.do_own = p.aligned_own;
+      a.pair = p.pair_aligned;
+      a.n_split = p.split_aligned;
+      a.units_per_view = ceil_div(d.max_q, a.pair ? MT : 2 * MT);
+      const dim3 grid((unsigned)(d.B * a.units_per_view * a.n_split), (unsigned)d.Hk);
+      view_attn_kernel<<<grid, kThreads, kSmemBytes, st>>>(mq, mkp, mvp, mko, mvo, a);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+  }
+  if (p.small_own) {
+    view_own_kernel<<<dim3((unsigned)d.B, (unsigned)d.Hk), 32 * OWN_WARPS, 0, st>>>(d, q, ko, vo, p.parts, part_o, part_lse,
+                                                                                  out, lse, err);
+    return cudaGetLastError();
+  }
+  if (p.parts > 0 || (!p.packed && !p.aligned)) {
+    const long long blocks = ((long long)d.n_q * d.H * 8 + 255) / 256;
+    merge_kernel<<<(unsigned)blocks, 256, 0, st>>>(d, p.parts, part_o, part_lse, out, lse);
+    return cudaGetLastError();
+  }
+  return cudaSuccess;
+}
+
+}  // namespace gsa

@@ -1,0 +1,57 @@
+// Launchers of the view-cache operators (prefix_attn, key_weights,
+// cache_evict), shared between their C-ABI layer and the kernel files.
+// Arguments are validated by the caller.
+#pragma once
+
+#include "internal.h"
+
+namespace gsa {
+
+// One batch of views: sizes, token strides (elements) and device offsets.
+struct ViewDims {
+  int B, H, Hk, G;           // views, query heads, key heads, query heads per key head
+  int n_q, n_own, n_prefix;  // tokens held by the buffers
+  int max_q, max_own;        // longest view: queries, own tokens
+  int causal;
+  long long q_stride, kp_stride, vp_stride, ko_stride, vo_stride, o_stride;
+  float scale, c2;           // softmax scale, and times log2(e)
+  long long wait_cycles;
+  const int* q_off;          // [B + 1] device
+  const int* own_off;        // [B + 1] device
+};
+
+// How a prefix_attn call is cut up (a function of the sizes alone).
+struct ViewPlan {
+  // the tensor-core launches: rows packed over views against the prefix
+  // alone, rows aligned to views against both, or against their own keys alone
+  int packed, aligned, aligned_prefix, aligned_own;
+  int small_own;   // the views' own keys by the CUDA-core kernel, which also merges
+  int pair_packed, pair_aligned;  // one row tile a CTA, its two slots taking alternate key tiles
+  int split_packed, split_aligned;  // key splits
+  int parts;       // partial results per (query, head); 0: written directly
+};
+ViewPlan view_plan(const ViewDims& d);
+
+cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16* q, const bf16* kp,
+                               const bf16* vp, const bf16* ko, const bf16* vo, bf16* out, float* lse,
+                               float* part_o, float* part_lse, unsigned* err, cudaStream_t st);
+
+// A view's ranges; false (and the device-check bit) when the offsets do not
+// describe rows of the buffers or more of them than a view may have.
+struct ViewRange {
+  int q0, q1, k0, k1;
+};
+__device__ __forceinline__ bool view_range(const ViewDims& d, int b, ViewRange* r, unsigned* err) {
+  r->q0 = d.q_off[b];
+  r->q1 = d.q_off[b + 1];
+  r->k0 = d.own_off[b];
+  r->k1 = d.own_off[b + 1];
+  if (r->q0 < 0 || r->q1 < r->q0 || r->q1 > d.n_q || r->q1 - r->q0 > d.max_q || r->k0 < 0 || r->k1 < r->k0 ||
+      r->k1 > d.n_own || r->k1 - r->k0 > d.max_own) {
+    atomicOr(err, kErrDeviceCheck);
+    return false;
+  }
+  return true;
+}
+
+}  // namespace gsa
