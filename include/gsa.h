@@ -428,6 +428,56 @@ gsa_status prefix_attn(const gsa_view_batch* batch, const gsa_bf16* q, const gsa
                        const int32_t* q_off, const int32_t* own_off, gsa_bf16* out, float* lse, void* ws,
                        size_t ws_bytes, void* stream);
 
+/*
+ * The account of attention received: for every key j and key head hk
+ *   w = sum over the queries i that see j, over the heads h of group hk, of
+ *       exp(scale * (q_ih . k_j) - lse[i][h]),
+ * i.e. the column sums of prefix_attn's weights, given its lse.  acc [Hk][acc_stride]
+ * is the account of the cached tokens; a row of acc_out [Hk][acc_out_stride] has
+ * room for n_prefix + n_own tokens, the own ones behind the cached ones in their
+ * order, as they would be appended:
+ *   acc_out[hk][j] = decay * acc[hk][j] + w        (j < n_prefix),
+ *   acc_out[hk][n_prefix + j] = w                  (own token j of a view).
+ * acc may be NULL (an account of zeros) or acc_out itself with its stride, and
+ * must not overlap it otherwise; it is not read when decay is 0.  decay is finite and >= 0.  An infinite entry stays infinite: the
+ * way to have a token never evicted.  A query whose lse is -infinity counts for
+ * nothing.  Slots of own tokens that belong to no view are not written.
+ * Sums are added in a fixed order: equal calls give equal bits.
+ */
+gsa_status key_weights(const gsa_view_batch* batch, const gsa_bf16* q, const gsa_bf16* k_prefix,
+                       const gsa_bf16* k_own, const int32_t* q_off, const int32_t* own_off, const float* lse,
+                       const float* acc, int64_t acc_stride, float* acc_out, int64_t acc_out_stride,
+                       float decay, void* ws, size_t ws_bytes, void* stream);
+
+/* One cache_evict call: n_tokens slots of the cache are in use, n_keep stay. */
+typedef struct {
+  int32_t n_kv_heads;  /* Hk in [1, 128] */
+  int32_t head_dim;    /* only 64 is built */
+  int32_t n_tokens;    /* >= 0 */
+  int32_t n_keep;      /* in [0, n_tokens] */
+  int32_t recent_from; /* tokens numbered this or later rank first, whatever their account */
+  int64_t k_stride, v_stride;  /* elements between tokens, 0 = dense */
+  int64_t w_stride;    /* elements between the heads' rows of acc, ids, acc_out and ids_out, >= n_tokens */
+} gsa_cache;
+
+/*
+ * Shrink a cache, head by head, to the n_keep tokens with the largest account.
+ * k, v [n_tokens][Hk][64]: changed in place.  acc, ids [Hk][w_stride]: the account
+ * and the number of the token in each slot (given by the caller: a count of the
+ * tokens ever appended, say).  Tokens numbered recent_from or later count as
+ * infinite; a NaN account counts as -infinity; equal ones go to the lower slot.
+ * Afterwards slots [0, n_keep) of k, v, acc_out and ids_out hold the kept tokens,
+ * each head's own choice.  A kept token below n_keep stays in its slot, and the
+ * r-th kept token at or behind n_keep is copied into the r-th free slot; slots at
+ * and behind n_keep of k and v keep what they hold, those of acc_out and ids_out
+ * are not written.  acc_out and ids_out must not overlap acc and ids, so the call
+ * may be repeated (it then does the same once more).
+ * ws: cache_workspace_size bytes.
+ */
+gsa_status cache_workspace_size(const gsa_cache* cache, size_t* bytes);
+gsa_status cache_evict(const gsa_cache* cache, gsa_bf16* k, gsa_bf16* v, const float* acc, const int32_t* ids,
+                       float* acc_out, int32_t* ids_out, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read the device error word in `ws`, clear it, and
  * return GSA_OK, GSA_ERR_TIMEOUT or GSA_ERR_DEVICE_CHECK.  For diagnosis, the
  * header's words 1 and 2 record the first in-kernel wait that ran out (its

@@ -34,6 +34,10 @@ from .api import (  # noqa: F401
 )
 from .views import (  # noqa: F401
     ViewBatch,
+    cache_evict,
+    cache_workspace_size,
+    key_weights,
+    new_cache_workspace,
     new_view_workspace,
     prefix_attn,
     view_workspace_size,

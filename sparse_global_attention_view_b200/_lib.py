@@ -78,10 +78,16 @@ class GsaViewBatch(ctypes.Structure):
                                       "v_own_stride", "out_stride")]
 
 
+class GsaCache(ctypes.Structure):
+    _fields_ = [(n, c_i32) for n in ("n_kv_heads", "head_dim", "n_tokens", "n_keep", "recent_from")] + [
+        (n, ctypes.c_int64) for n in ("k_stride", "v_stride", "w_stride")]
+
+
 FORWARD_STEPS = ("pool", "compressed_attn", "block_scores", "topk_merge", "kept_attn", "selected_gate")
 
 P_SHAPE = ctypes.POINTER(GsaShape)
 P_VIEWS = ctypes.POINTER(GsaViewBatch)
+P_CACHE = ctypes.POINTER(GsaCache)
 
 # name -> argument types (all return gsa_status, an int, except gsa_status_string)
 SIGNATURES = {
@@ -106,6 +112,9 @@ SIGNATURES = {
     "gsa_noalloc_check_device_error": [c_vp],
     "view_workspace_size": [P_VIEWS, ctypes.POINTER(c_size)],
     "prefix_attn": [P_VIEWS] + [c_vp] * 10 + [c_size, c_vp],
+    "key_weights": [P_VIEWS] + [c_vp] * 7 + [ctypes.c_int64, c_vp, ctypes.c_int64, c_f32, c_vp, c_size, c_vp],
+    "cache_workspace_size": [P_CACHE, ctypes.POINTER(c_size)],
+    "cache_evict": [P_CACHE] + [c_vp] * 7 + [c_size, c_vp],
     "gsa_check_device_error": [c_vp, c_vp],
     "gsa_selftest_exp2": [c_vp, c_vp, ctypes.c_int64, c_vp],
     "gsa_status_string": [c_i32],

@@ -1,0 +1,582 @@
+// How much attention every key received: the column sums of a softmax whose row
+// sums are known,
+//   w[hk][j] = sum over queries i that see j, over the heads h of group hk, of
+//              exp(scale q_ih . k_j - lse_ih),
+// added to a running account of the cached keys.
+//
+// key_weights_kernel (tcgen05 / TMEM / TMA): the products are taken transposed,
+// S^T = K Q^T with 128 keys as the rows of a tile, so a thread owns a key and its
+// sum stays in a register; no atomics, and no reduction over lanes.  A work item
+// is 512 keys of one key head (four tiles) against a range of query tiles (128
+// (token, head of the group) rows each); one CTA an SM takes items in turn:
+//   warp 0       TMA producer: the item's key tiles (two sets of four, so the next
+//                item's keys arrive during this one) and a 5-stage ring of query tiles;
+//   warp 1       MMA issuer: for each query tile four products, one a key tile;
+//   warp 2       the query tile's -lse log2(e) into the ring (and TMEM allocation);
+//   warps 4-19   a warpgroup for each key tile: exponentials and sums.
+// While one warpgroup waits for its product the three others have the
+// exponential units busy: those bound it (half as many tensor flops an
+// exponential as in attention, and no maximum, packing or store of weights).
+// Few items are cut over query ranges, whose sums are added in order afterwards.
+//
+// key_weights_rows_kernel: at most eight rows in all.  Bound by the read of the
+// keys; eight lanes hold a key, and after the dot products lane r takes the
+// exponential of row r.
+//
+// All sums are fp32: a tile's 128 terms in 8 chains, then tile after tile.
+#include <math_constants.h>
+
+#include "exp2_poly.cuh"
+#include "views.h"
+
+namespace gsa {
+namespace {
+
+using namespace tc;
+
+constexpr int kPolyOf8 = 2;  // pairs of exponentials in eight on the FMA pipe
+constexpr int SLOTS = 4;     // key tiles of an item
+constexpr int ITEM = 128 * SLOTS;
+constexpr int ST = 5;        // query ring stages
+constexpr int kThreads = 128 + 128 * SLOTS;
+constexpr uint32_t kTile = 128 * 128;
+
+constexpr uint32_t OFF_K = 0;
+constexpr uint32_t OFF_Q = OFF_K + 2 * SLOTS * kTile;
+constexpr uint32_t OFF_L = OFF_Q + ST * kTile;
+constexpr uint32_t OFF_BAR = OFF_L + ST * 512;
+constexpr uint32_t OFF_MISC = OFF_BAR + 256;
+constexpr uint32_t kSmemBytes = OFF_MISC + 64 + 1024;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+
+// KF/KE: a set of key tiles filled / free; QF/QE: a query stage; LF: its lse; SF/SE: a score tile
+constexpr int B_KF = 0, B_KE = B_KF + 2, B_QF = B_KE + 2, B_QE = B_QF + ST, B_LF = B_QE + ST, B_SF = B_LF + ST,
+              B_SE = B_SF + SLOTS, B_DRAIN = B_SE + SLOTS, B_COUNT = B_DRAIN + 1;
+static_assert(B_COUNT * 8 <= 256, "barrier area");
+constexpr uint32_t kCols = 128 * SLOTS;
+
+struct WeightsArgs {
+  ViewDims d;
+  int rows_tok;                       // tokens per query tile: 128 / G
+  int prefix_units, own_units;        // items of 512 keys: of the prefix, of one view at most
+  int split_prefix, split_own;        // query ranges of an item
+  int n_items;
+  const float* lse;                   // [n_q][H]
+  const float* acc;                   // nullable [Hk][acc_stride]
+  float* acc_out;                     // [Hk][acc_out_stride]
+  float decay;
+  long long acc_stride, acc_out_stride;
+  float* part_prefix;                 // [split_prefix][Hk][n_prefix] when split_prefix > 1
+  float* part_own;                    // [split_own][Hk][n_own] when split_own > 1
+  unsigned* err;
+};
+
+// One work item; n_keys = 0: nothing to do.
+struct Item {
+  int hk, own, split;
+  int key0, n_keys;  // rows of the prefix or of the own keys
+  int tok0;          // first token of the first query tile
+  int tiles;         // query tiles
+  int tok_lo, tok_hi;  // tokens that see the keys, apart from causal masks
+  int see0;          // causal: key key0 + r is seen by tokens >= see0 + r
+};
+
+__device__ __forceinline__ Item get_item(const WeightsArgs& a, int idx, bool report) {
+  const ViewDims& d = a.d;
+  Item it;
+  const int per_head = a.prefix_units * a.split_prefix + d.B * a.own_units * a.split_own;
+  it.hk = idx / per_head;
+  int r = idx - it.hk * per_head;
+  it.n_keys = 0;
+  it.tiles = 0;
+  it.see0 = -2147483647;
+  int n_split;
+  it.own = r >= a.prefix_units * a.split_prefix;
+  if (!it.own) {
+    n_split = a.split_prefix;
+    it.split = r / a.prefix_units;
+    it.key0 = (r - it.split * a.prefix_units) * ITEM;
+    it.n_keys = min(ITEM, d.n_prefix - it.key0);
+    it.tok_lo = max(d.q_off[0], 0);
+    it.tok_hi = min(d.q_off[d.B], d.n_q);
+    it.tok0 = 0;
+  } else {
+    r -= a.prefix_units * a.split_prefix;
+    n_split = a.split_own;
+    it.split = r / (d.B * a.own_units);
+    r -= it.split * d.B * a.own_units;
+    const int b = r / a.own_units, u = r - b * a.own_units;
+    ViewRange v;
+    if (report ? !view_range(d, b, &v, a.err) : !view_range(d, b, &v, nullptr)) return it;
+    const int nk = v.k1 - v.k0, nq = v.q1 - v.q0;
+    if (u * ITEM >= nk) return it;
+    it.key0 = v.k0 + u * ITEM;
+    it.n_keys = min(ITEM, nk - u * ITEM);
+    it.tok_lo = it.tok0 = v.q0;
+    it.tok_hi = v.q1;
+    if (d.causal) {
+      // key j of the view is seen by its queries i >= j + nq - nk
+      it.see0 = v.q0 + u * ITEM + nq - nk;
+      it.tok0 += max(0, it.see0 - v.q0) / a.rows_tok * a.rows_tok;
+    }
+  }
+  const int all = max(0, (it.tok_hi - it.tok0 + a.rows_tok - 1) / a.rows_tok);
+  const int t0 = (int)((long long)all * it.split / n_split);
+  it.tiles = (int)((long long)all * (it.split + 1) / n_split) - t0;
+  it.tok0 += t0 * a.rows_tok;
+  return it;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    key_weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tkp,
+                       const __grid_constant__ CUtensorMap tko, const WeightsArgs a) {
+  extern __shared__ __align__(1024) uint8_t tc_smem_raw[];
+  const uint32_t raw = smem_u32(tc_smem_raw);
+  const uint32_t sb = (raw + 1023u) & ~1023u;
+  uint8_t* sp = tc_smem_raw + (sb - raw);
+  const uint32_t sK = sb + OFF_K, sQ = sb + OFF_Q;
+  auto bar = [&](int i) -> uint32_t { return sb + OFF_BAR + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + OFF_MISC + 4);
+  float* sL = reinterpret_cast<float*>(sp + OFF_L);
+
+  const ViewDims& d = a.d;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int MT = a.rows_tok, tile_rows = MT * d.G;
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(B_KF + s), 1);
+      mbar_init(bar(B_KE + s), 1);
+    }
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(bar(B_QF + s), 1);
+      mbar_init(bar(B_QE + s), 1 + 4 * SLOTS);  // the products, and every sum warp
+      mbar_init(bar(B_LF + s), 1);
+    }
+    for (int t = 0; t < SLOTS; ++t) {
+      mbar_init(bar(B_SF + t), 1);
+      mbar_init(bar(B_SE + t), 4);
+    }
+    mbar_init(bar(B_DRAIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // rows of the ring that no copy fills (group sizes that do not divide 128)
+  for (int s = 0; s < ST; ++s)
+    for (uint32_t o = tile_rows * 128u + tid * 16u; o < kTile; o += kThreads * 16u)
+      *reinterpret_cast<uint4*>(sp + OFF_Q + s * kTile + o) = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  if (warp == 2) {
+    tmem_alloc(smem_u32(tmem_slot), kCols);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tbase = *tmem_slot;
+  const long long limit = d.wait_cycles;
+  auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, a.err, limit); };
+
+  // every role walks the same items; `it_n` counts those with products, `step`
+  // the query tiles of all of them
+  if (warp == 0) {
+    if (lane == 0) {
+      int it_n = 0, step = 0;
+      bool ok = true;
+      for (int idx = blockIdx.x; ok && idx < a.n_items; idx += gridDim.x) {
+        const Item it = get_item(a, idx, true);
+        if (it.n_keys == 0 || it.tiles == 0) continue;
+        const int kb = it_n & 1, slots = (it.n_keys + 127) / 128;
+        if (it_n >= 2 && !(ok = wait(B_KE + kb, ((it_n >> 1) - 1) & 1))) break;
+        mbar_expect_tx(bar(B_KF + kb), slots * kTile);
+        for (int t = 0; t < slots; ++t)
+          tma_load_3d(sK + (kb * SLOTS + t) * kTile, it.own ? &tko : &tkp, bar(B_KF + kb), 0, it.hk, it.key0 + t * 128);
+        ++it_n;
+        for (int i = 0; i < it.tiles; ++i, ++step) {
+          const int s = step % ST;
+          if (step >= ST && !(ok = wait(B_QE + s, (step / ST - 1) & 1))) break;
+          mbar_expect_tx(bar(B_QF + s), tile_rows * 128u);
+          tma_load_3d(sQ + s * kTile, &tq, bar(B_QF + s), 0, it.hk * d.G, it.tok0 + i * MT);
+        }
+      }
+      // this CTA's own copies land before its shared memory goes away, whatever
+      // becomes of the other warps
+      volatile int never = 0;
+      for (int k = max(0, it_n - 2); k < it_n; ++k) mbar_wait(bar(B_KF + (k & 1)), (k >> 1) & 1, &never, a.err);
+      for (int k = max(0, step - ST); k < step; ++k) mbar_wait(bar(B_QF + k % ST), (k / ST) & 1, &never, a.err);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = idesc(128, 128, kFmtBF16, 0, 0);
+      int it_n = 0, step = 0;
+      uint32_t se_seen = 0;  // a bit for each slot: parity of its next free-wait
+      uint32_t se_used = 0;  // slots that have been written before
+      bool ok = true;
+      for (int idx = blockIdx.x; ok && idx < a.n_items; idx += gridDim.x) {
+        const Item it = get_item(a, idx, false);
+        if (it.n_keys == 0 || it.tiles == 0) continue;
+        const int kb = it_n & 1, slots = (it.n_keys + 127) / 128;
+        if (!(ok = wait(B_KF + kb, (it_n >> 1) & 1))) break;
+        for (int i = 0; ok && i < it.tiles; ++i, ++step) {
+          const int s = step % ST;
+          if (!(ok = wait(B_QF + s, (step / ST) & 1))) break;
+          for (int t = 0; t < slots; ++t) {
+            if (se_used >> t & 1) {
+              if (!(ok = wait(B_SE + t, se_seen >> t & 1))) break;
+              se_seen ^= 1u << t;
+            }
+            se_used |= 1u << t;
+            fence_after_sync();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ss(tbase + t * 128, sdesc_k(sK + (kb * SLOTS + t) * kTile + kk * 32),
+                          sdesc_k(sQ + s * kTile + kk * 32), id, kk > 0);
+            mma_commit(bar(B_SF + t));
+          }
+          if (ok) mma_commit(bar(B_QE + s));
+        }
+        if (ok) mma_commit(bar(B_KE + kb));
+        ++it_n;
+      }
+      if (!ok) {
+        // wait for the products already issued before TMEM is released
+        volatile int never = 0;
+        mma_commit(bar(B_DRAIN));
+        mbar_wait(bar(B_DRAIN), 0, &never, a.err);
+      }
+    }
+  } else if (warp == 2) {
+    int step = 0;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += gridDim.x) {
+      const Item it = get_item(a, idx, false);
+      if (it.n_keys == 0) continue;
+      for (int i = 0; ok && i < it.tiles; ++i, ++step) {
+        const int s = step % ST;
+        const int tok0 = it.tok0 + i * MT;
+        float v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = u * 32 + lane, tl = row / d.G, tok = tok0 + tl;
+          // rows of no token weigh nothing, as do queries that saw no key
+          v[u] = -CUDART_INF_F;
+          if (tl < MT && tok >= it.tok_lo && tok < it.tok_hi) {
+            const float z = a.lse[(long long)tok * d.H + it.hk * d.G + row - tl * d.G];
+            if (z != -CUDART_INF_F) v[u] = -z * 1.4426950408889634f;
+          }
+        }
+        if (step >= ST && !(ok = __all_sync(0xffffffffu, wait(B_QE + s, (step / ST - 1) & 1)))) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sL[s * 128 + u * 32 + lane] = v[u];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_LF + s));
+      }
+    }
+  } else if (warp >= 4) {
+    const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t s_addr = tbase + ((uint32_t)((warp & 3) * 32) << 16) + t * 128;
+    const float c2 = d.c2;
+    const uint64_t c2p = f2_pack(c2, c2);
+    int step = 0;
+    uint32_t sf = 0;  // parity of the slot's next product
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += gridDim.x) {
+      const Item it = get_item(a, idx, false);
+      if (it.n_keys == 0) continue;
+      const int r = t * 128 + row;  // the thread's key of the item
+      const bool slot_live = t * 128 < it.n_keys;
+      float total = 0.f;
+      for (int i = 0; ok && i < it.tiles; ++i, ++step) {
+        const int s = step % ST;
+        ok = __all_sync(0xffffffffu, wait(B_LF + s, (step / ST) & 1));
+        if (!ok) break;
+        if (slot_live) {
+          ok = __all_sync(0xffffffffu, wait(B_SF + t, sf));
+          if (!ok) break;
+          sf ^= 1;
+          fence_after_sync();
+          // rows [lo, hi) of the tile see this key
+          const int tok0 = it.tok0 + i * MT;
+          const int lo = max(max(it.tok_lo, it.see0 + r) - tok0, 0) * d.G;
+          const int hi = it.tok_hi - tok0 >= MT ? 128 : (it.tok_hi - tok0) * d.G;
+          const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == 128);
+          const float4* nl = reinterpret_cast<const float4*>(sL + s * 128);
+          uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t sv[32];
+            tmem_ld32(s_addr + 32 * c, sv);
+            tmem_wait_ld();
+            if (c == 3) {
+              fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(B_SE + t));
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const float4 z = nl[8 * c + u];
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const int k = 4 * u + 2 * w;
+                const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2p,
+                                           w ? f2_pack(z.z, z.w) : f2_pack(z.x, z.y));
+                uint64_t p2;
+                if (((2 * u + w) & 7) >= 8 - kPolyOf8) {
+                  p2 = exp2_poly2(x2);
+                } else {
+                  float x0, x1;
+                  f2_unpack(x2, x0, x1);
+                  p2 = f2_pack(exp2_mufu(x0), exp2_mufu(x1));
+                }
+                if (!whole) {
+                  float p0, p1;
+                  f2_unpack(p2, p0, p1);
+                  const int col = 32 * c + k;
+                  p2 = f2_pack(col >= lo && col < hi ? p0 : 0.f, col + 1 >= lo && col + 1 < hi ? p1 : 0.f);
+                }
+                ps[(2 * u + w) & 3] = f2_add(ps[(2 * u + w) & 3], p2);
+              }
+            }
+          }
+          const uint64_t p01 = f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3]));
+          float p0, p1;
+          f2_unpack(p01, p0, p1);
+          total += p0 + p1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_QE + s));
+      }
+      if (ok && r < it.n_keys) {
+        const int key = it.key0 + r;
+        const int n_split = it.own ? a.split_own : a.split_prefix;
+        if (n_split > 1) {
+          if (it.own)
+            a.part_own[((long long)it.split * d.Hk + it.hk) * d.n_own + key] = total;
+          else
+            a.part_prefix[((long long)it.split * d.Hk + it.hk) * d.n_prefix + key] = total;
+        } else {
+          if (!it.own && a.acc) total += a.decay * a.acc[it.hk * a.acc_stride + key];
+          a.acc_out[it.hk * a.acc_out_stride + (it.own ? d.n_prefix + key : key)] = total;
+        }
+      }
+    }
+  }
+  fence_before_sync();
+  __syncthreads();
+  if (warp == 2) {
+    fence_after_sync();
+    tmem_dealloc(tbase, kCols);
+  }
+}
+
+// The sums of query ranges, in order; key j of the cache and the own keys.
+__global__ void __launch_bounds__(256) add_parts_kernel(const WeightsArgs a) {
+  const ViewDims& d = a.d;
+  const int j = blockIdx.x * 256 + threadIdx.x, hk = blockIdx.y;
+  const long long at = hk * a.acc_out_stride + j;
+  if (j < d.n_prefix) {
+    if (a.split_prefix < 2) return;
+    float t = 0.f;
+    for (int s = 0; s < a.split_prefix; ++s) t += a.part_prefix[((long long)s * d.Hk + hk) * d.n_prefix + j];
+    if (a.acc) t += a.decay * a.acc[hk * a.acc_stride + j];
+    a.acc_out[at] = t;
+  } else if (j < d.n_prefix + d.n_own) {
+    const int k = j - d.n_prefix;
+    if (a.split_own < 2 || k < d.own_off[0] || k >= d.own_off[d.B]) return;
+    float t = 0.f;
+    for (int s = 0; s < a.split_own; ++s) t += a.part_own[((long long)s * d.Hk + hk) * d.n_own + k];
+    a.acc_out[at] = t;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// at most eight rows
+
+constexpr int ROWS = 8;
+constexpr int KEYS_BLOCK = 128;  // keys of a block: 32 groups of eight lanes, four keys each
+
+__device__ __forceinline__ float dot8(const uint4& u, const float (&q)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(w[i] << 16), q[2 * i], s);
+    s = fmaf(__uint_as_float(w[i] & 0xffff0000u), q[2 * i + 1], s);
+  }
+  return s;
+}
+
+__global__ void __launch_bounds__(256)
+    key_weights_rows_kernel(const WeightsArgs a, const bf16* __restrict__ q, const bf16* __restrict__ kp,
+                            const bf16* __restrict__ ko, int prefix_blocks) {
+  const ViewDims& d = a.d;
+  const int hk = blockIdx.y, grp = threadIdx.x >> 3, e = threadIdx.x & 7;
+  const bool own = (int)blockIdx.x >= prefix_blocks;
+  const int key0 = ((int)blockIdx.x - (own ? prefix_blocks : 0)) * KEYS_BLOCK;
+  const int n_keys = own ? d.n_own : d.n_prefix;
+  const bf16* k = own ? ko : kp;
+  const long long stride = own ? d.ko_stride : d.kp_stride;
+  const int rows = d.n_q * d.G;
+  if (blockIdx.x == 0 && hk == 0) {
+    ViewRange r;
+    for (int b = threadIdx.x; b < d.B; b += 256) view_range(d, b, &r, a.err);
+  }
+  uint4 ku[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int j = key0 + u * 32 + grp;
+    ku[u] = j < n_keys ? *reinterpret_cast<const uint4*>(k + j * stride + hk * 64 + e * 8) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float qf[ROWS][8];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int row = min(i, rows - 1), tl = row / d.G, h = hk * d.G + row - tl * d.G;
+    const uint4 w = *reinterpret_cast<const uint4*>(q + tl * d.q_stride + h * 64 + e * 8);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      qf[i][2 * c] = __uint_as_float(x[c] << 16);
+      qf[i][2 * c + 1] = __uint_as_float(x[c] & 0xffff0000u);
+    }
+  }
+  // lane e looks after row e
+  const int my_tok = e / d.G;
+  float nl = -CUDART_INF_F;
+  if (e < rows) {
+    const float z = a.lse[(long long)my_tok * d.H + hk * d.G + e - my_tok * d.G];
+    if (z != -CUDART_INF_F) nl = -z * 1.4426950408889634f;
+  }
+  int tok_lo = max(d.q_off[0], 0), tok_hi = min(d.q_off[d.B], d.n_q);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int j = key0 + u * 32 + grp;
+    bool write = j < n_keys;
+    if (own) {
+      // the view of the key: the last one that starts at or before it
+      int lo = 0, hi = d.B;  // own_off[lo] <= j < own_off[hi], once it holds at all
+      write = write && j >= d.own_off[0] && j < d.own_off[d.B];
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (d.own_off[mid] <= j) lo = mid; else hi = mid;
+      }
+      tok_lo = max(d.q_off[lo], 0);
+      tok_hi = min(d.q_off[lo + 1], d.n_q);
+      if (d.causal) tok_lo = max(tok_lo, j - d.own_off[lo + 1] + d.q_off[lo + 1]);
+    }
+    float mine = 0.f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (i >= rows) break;
+      float s = dot8(ku[u], qf[i]);
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      s += __shfl_xor_sync(0xffffffffu, s, 4);
+      if (i == e) mine = s;
+    }
+    float p = e < rows && my_tok >= tok_lo && my_tok < tok_hi ? exp2_mufu(fmaf(mine, d.c2, nl)) : 0.f;
+    p += __shfl_xor_sync(0xffffffffu, p, 1);
+    p += __shfl_xor_sync(0xffffffffu, p, 2);
+    p += __shfl_xor_sync(0xffffffffu, p, 4);
+    if (write && e == 0) {
+      if (!own && a.acc) p += a.decay * a.acc[hk * a.acc_stride + j];
+      a.acc_out[hk * a.acc_out_stride + (own ? d.n_prefix + j : j)] = p;
+    }
+  }
+}
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+}  // namespace
+
+WeightsPlan weights_plan(const ViewDims& d) {
+  WeightsPlan p = {};
+  p.split_prefix = p.split_own = 1;
+  if ((long long)d.n_q * d.G <= ROWS && d.n_q > 0) {
+    p.rows = 1;
+    return p;
+  }
+  const int MT = 128 / d.G;
+  p.prefix_units = ceil_div(d.n_prefix, ITEM);
+  p.own_units = ceil_div(d.max_own, ITEM);
+  // query ranges so that the items fill the SMs evenly: an item costs its query
+  // tiles and about two more, and there are as many own items as tokens at most
+  const int tiles_p = ceil_div(d.n_q, MT), tiles_o = ceil_div(d.max_q, MT);
+  long long own_items = (long long)d.B * p.own_units;
+  if (own_items > d.n_own / ITEM + d.B) own_items = d.n_own / ITEM + d.B;
+  double best = 0;
+  for (int s = 1; s <= 32 && s <= (tiles_p > 1 ? tiles_p : 1); ++s) {
+    const int per_p = ceil_div(tiles_p, s), so = per_p > 0 ? ceil_div(tiles_o, per_p) : 1;
+    const double items = ((double)p.prefix_units * s + (double)own_items * so) * d.Hk;
+    const double work = ((double)p.prefix_units * s * (per_p + 2.0) + (double)own_items * so * (ceil_div(tiles_o, so) + 2.0)) * d.Hk;
+    const double longest = (per_p > ceil_div(tiles_o, so) ? per_p : ceil_div(tiles_o, so)) + 2.0;
+    const double cost = work / 148.0 + (items > 148.0 ? 0.5 : 1.0) * longest + (s > 1 ? 6.0 : 0.0);
+    if (s == 1 || cost < best) {
+      best = cost;
+      p.split_prefix = s;
+      p.split_own = so > 1 ? so : 1;
+    }
+  }
+  return p;
+}
+
+cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf16* q, const bf16* kp, const bf16* ko,
+                               const float* lse, const float* acc, long long acc_stride, float* acc_out,
+                               long long acc_out_stride, float decay, float* part_prefix, float* part_own, unsigned* err, cudaStream_t st) {
+  if (d.n_prefix + d.n_own <= 0) return cudaSuccess;
+  WeightsArgs a = {};
+  a.d = d;
+  a.lse = lse;
+  a.acc = decay != 0.f ? acc : nullptr;
+  a.acc_out = acc_out;
+  a.decay = decay;
+  a.acc_stride = acc_stride;
+  a.acc_out_stride = acc_out_stride;
+  a.part_prefix = part_prefix;
+  a.part_own = part_own;
+  a.err = err;
+  if (p.rows) {
+    const int pb = ceil_div(d.n_prefix, KEYS_BLOCK), ob = ceil_div(d.n_own, KEYS_BLOCK);
+    key_weights_rows_kernel<<<dim3((unsigned)(pb + ob), (unsigned)d.Hk), 256, 0, st>>>(a, q, kp, ko, pb);
+    return cudaGetLastError();
+  }
+  const int MT = 128 / d.G;
+  a.rows_tok = MT;
+  a.prefix_units = p.prefix_units;
+  a.own_units = p.own_units;
+  a.split_prefix = p.split_prefix;
+  a.split_own = p.split_own;
+  const long long items = ((long long)p.prefix_units * p.split_prefix + (long long)d.B * p.own_units * p.split_own) * d.Hk;
+  if (items > 0x7fffffffLL - 1024) return cudaErrorInvalidValue;
+  a.n_items = (int)items;
+  if (a.n_items > 0) {
+    cudaError_t e = cudaFuncSetAttribute(key_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mq, mkp, mko;
+    auto map = [&](CUtensorMap* m, const bf16* base, int heads, int rows, long long stride, int b1, int b2) {
+      return make_tmap_3d(m, false, base, 64, (unsigned long long)heads, (unsigned long long)rows, 128,
+                          (unsigned long long)stride * 2, 64, (unsigned)b1, (unsigned)b2);
+    };
+    bool ok = true;
+    if (d.n_prefix > 0) ok = ok && map(&mkp, kp, d.Hk, d.n_prefix, d.kp_stride, 1, 128);
+    if (d.n_own > 0) ok = ok && map(&mko, ko, d.Hk, d.n_own, d.ko_stride, 1, 128);
+    // a map that no item uses still has to be one
+    if (d.n_prefix <= 0) mkp = mko;
+    if (d.n_own <= 0) mko = mkp;
+    if (d.n_q > 0)
+      ok = ok && map(&mq, q, d.H, d.n_q, d.q_stride, d.G, MT);
+    else
+      mq = mkp;
+    if (!ok) return cudaErrorInvalidValue;
+    const int grid = a.n_items < 148 ? a.n_items : 148;
+    key_weights_kernel<<<(unsigned)grid, kThreads, kSmemBytes, st>>>(mq, mkp, mko, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.split_prefix > 1 || p.split_own > 1) {
+    add_parts_kernel<<<dim3((unsigned)ceil_div((long long)d.n_prefix + d.n_own, 256), (unsigned)d.Hk), 256, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  return cudaSuccess;
+}
+
+}  // namespace gsa

@@ -36,6 +36,27 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
                                const bf16* vp, const bf16* ko, const bf16* vo, bf16* out, float* lse,
                                float* part_o, float* part_lse, unsigned* err, cudaStream_t st);
 
+// How a key_weights call is cut up.
+struct WeightsPlan {
+  int rows;  // at most eight rows: the kernel for those
+  int prefix_units, own_units;    // work items of 512 keys: of the prefix, of one view at most
+  int split_prefix, split_own;    // query ranges of an item
+};
+WeightsPlan weights_plan(const ViewDims& d);
+
+cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf16* q, const bf16* kp, const bf16* ko,
+                               const float* lse, const float* acc, long long acc_stride, float* acc_out,
+                               long long acc_out_stride, float decay, float* part_prefix, float* part_own, unsigned* err, cudaStream_t st);
+
+// One cache_evict call.
+struct EvictDims {
+  int Hk, n, keep, recent_from;
+  long long k_stride, v_stride, w_stride;  // elements
+};
+inline int evict_most_moves(const EvictDims& d) { return d.keep < d.n - d.keep ? d.keep : d.n - d.keep; }
+cudaError_t launch_cache_evict(const EvictDims& d, bf16* k, bf16* v, const float* acc, const int* ids, float* acc_out,
+                               int* ids_out, int* n_moves, int* src, int* dst, cudaStream_t st);
+
 // A view's ranges; false (and the device-check bit) when the offsets do not
 // describe rows of the buffers or more of them than a view may have.
 struct ViewRange {
@@ -48,7 +69,7 @@ __device__ __forceinline__ bool view_range(const ViewDims& d, int b, ViewRange* 
   r->k1 = d.own_off[b + 1];
   if (r->q0 < 0 || r->q1 < r->q0 || r->q1 > d.n_q || r->q1 - r->q0 > d.max_q || r->k0 < 0 || r->k1 < r->k0 ||
       r->k1 > d.n_own || r->k1 - r->k0 > d.max_own) {
-    atomicOr(err, kErrDeviceCheck);
+    if (err) atomicOr(err, kErrDeviceCheck);
     return false;
   }
   return true;

@@ -13,7 +13,7 @@ from dataclasses import dataclass
 
 import torch
 
-from ._lib import GsaViewBatch, check, load
+from ._lib import GsaCache, GsaViewBatch, check, load
 from .api import BF16, F32, I32, WS_HEADER_BYTES
 
 
@@ -101,6 +101,15 @@ class _Call:
             raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)} strides {t.stride()}")
         return t.data_ptr()
 
+    def table(self, t, dtype, heads, least, name, optional=False):
+        """Pointer and row stride of [heads][>= least] with dense rows."""
+        if t is None and optional:
+            return None, 0
+        self._tensor(t, dtype, name)
+        if t.dim() != 2 or t.shape[0] != heads or t.shape[1] < least or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be [{heads}, >= {least}] with dense rows, got {tuple(t.shape)} strides {t.stride()}")
+        return t.data_ptr(), t.stride(0) if heads > 1 else t.shape[1]
+
     def run(self, fn, where, stream, *args):
         if torch.cuda.current_device() == self.device.index:
             st = torch.cuda.current_stream() if stream is None else stream
@@ -130,3 +139,64 @@ def prefix_attn(batch: ViewBatch, q, k_prefix, v_prefix, k_own, v_own, q_off, ow
     c.run(load().prefix_attn, "prefix_attn", stream, ctypes.byref(b), pq, pkp, pvp, pko, pvo,
           c.flat(q_off, I32, offs, "q_off"), c.flat(own_off, I32, offs, "own_off"), pout,
           c.flat(lse, F32, (b.n_q, H), "lse", True), ws.data_ptr(), c.ws_bytes)
+
+
+def key_weights(batch: ViewBatch, q, k_prefix, k_own, q_off, own_off, lse, acc, acc_out, decay: float, ws,
+                stream=None) -> None:
+    """Adds the attention every key received (the column sums of prefix_attn's weights, given its lse) to an account.
+
+    acc_out [Hk, >= n_prefix + n_own] float32 gets decay * acc + the sums for the cached tokens and the sums for the
+    own tokens behind them; acc [Hk, >= n_prefix] may be None (zeros) or acc_out itself.
+    """
+    c, b = _Call(ws), batch.c()
+    D, H, Hk = batch.head_dim, b.n_heads, b.n_kv_heads
+    pq, b.q_stride = c.rows(q, b.n_q, H, D, "q")
+    pkp, b.k_prefix_stride = c.rows(k_prefix, b.n_prefix, Hk, D, "k_prefix")
+    pko, b.k_own_stride = c.rows(k_own, b.n_own, Hk, D, "k_own")
+    offs = (b.n_views + 1,)
+    pout, out_stride = c.table(acc_out, F32, Hk, b.n_prefix + b.n_own, "acc_out")
+    pacc, acc_stride = c.table(acc, F32, Hk, b.n_prefix, "acc", True)
+    c.run(load().key_weights, "key_weights", stream, ctypes.byref(b), pq, pkp, pko, c.flat(q_off, I32, offs, "q_off"),
+          c.flat(own_off, I32, offs, "own_off"), c.flat(lse, F32, (b.n_q, H), "lse"), pacc, acc_stride, pout, out_stride,
+          decay, ws.data_ptr(), c.ws_bytes)
+
+
+def _cache(n_kv_heads: int, n_tokens: int, n_keep: int, recent_from: int = 0) -> GsaCache:
+    return GsaCache(n_kv_heads, 64, n_tokens, n_keep, recent_from, 0, 0, n_tokens)
+
+
+def cache_workspace_size(n_kv_heads: int, n_tokens: int, n_keep: int) -> int:
+    n = ctypes.c_size_t()
+    check(load().cache_workspace_size(ctypes.byref(_cache(n_kv_heads, n_tokens, n_keep)), ctypes.byref(n)),
+          "cache_workspace_size")
+    return n.value
+
+
+def new_cache_workspace(n_kv_heads: int, n_tokens: int, n_keep: int, device=None, stream=None) -> torch.Tensor:
+    """Zero-headed workspace for cache_evict.  Calls that share it must be ordered."""
+    return _new_workspace(cache_workspace_size(n_kv_heads, n_tokens, n_keep), device, stream)
+
+
+def cache_evict(n_tokens: int, n_keep: int, recent_from: int, k, v, acc, ids, acc_out, ids_out, ws,
+                stream=None) -> None:
+    """Shrinks a cache to the n_keep tokens of each head with the largest account (gsa.h).
+
+    k, v [>= n_tokens, Hk, 64] bf16 are changed in place; acc, acc_out float32 and ids, ids_out int32 are
+    [Hk, >= n_tokens] with one row stride.  Afterwards the first n_keep slots of k, v, acc_out and ids_out are the cache.
+    Tokens whose number is recent_from or more rank first.
+    """
+    c = _Call(ws)
+    for t, name in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[0] < n_tokens:
+            raise ValueError(f"{name} must be [>= {n_tokens}, heads, 64]")
+    Hk = k.shape[1]
+    b = _cache(Hk, n_tokens, n_keep, recent_from)
+    pk, b.k_stride = c.rows(k[:n_tokens], n_tokens, Hk, 64, "k")
+    pv, b.v_stride = c.rows(v[:n_tokens], n_tokens, Hk, 64, "v")
+    tables = [c.table(t, dt, Hk, n_tokens, name) for t, dt, name in
+              ((acc, F32, "acc"), (ids, I32, "ids"), (acc_out, F32, "acc_out"), (ids_out, I32, "ids_out"))]
+    if len({s for _, s in tables}) != 1:
+        raise ValueError(f"acc, ids, acc_out and ids_out must have one row stride, got {[s for _, s in tables]}")
+    b.w_stride = tables[0][1]
+    c.run(load().cache_evict, "cache_evict", stream, ctypes.byref(b), pk, pv, *[p for p, _ in tables], ws.data_ptr(),
+          c.ws_bytes)

@@ -98,3 +98,111 @@ def test_attend(name, causal):
     x = make(*SIZES[name], seed=len(name))
     out, lse = attend(x, batch_of(x, causal))
     assert_attend(x, out, lse, causal)
+
+
+def weigh(x, batch, lse, acc, decay, acc_out=None, ws=None, stream=None):
+    ws = G().new_view_workspace(batch) if ws is None else ws
+    Hk, n = x["kp"].shape[1], x["kp"].shape[0] + x["ko"].shape[0]
+    acc_out = torch.full((Hk, n), 7.0, device=DEV) if acc_out is None else acc_out
+    G().key_weights(batch, x["q"], x["kp"], x["ko"], ints(x["q_off"]), ints(x["own_off"]), lse, acc, acc_out, decay, ws,
+                    stream)
+    G().check_device_error(ws)
+    return acc_out
+
+
+def exact_lse(x, causal=False):
+    z = R.attend(x["q"], x["kp"], x["vp"], x["ko"], x["vo"], x["q_off"], x["own_off"], causal)[1]
+    return z.nan_to_num(0.0, neginf=R.NEG).float()
+
+
+def assert_weights(x, got, lse, acc, decay, causal=False):
+    w, tol = R.weights(x["q"], x["kp"], x["ko"], x["q_off"], x["own_off"], lse, acc, decay, causal)
+    there = ~w.isnan()
+    d = (got[:, :w.shape[1]].double() - w).abs()[there]
+    assert (d <= tol[there]).all(), f"{d.max().item():.3e}: {(d / tol[there]).max().item():.2f} of the bound"
+    assert (got[:, :w.shape[1]][~there] == 7).all()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("name", list(SIZES))
+def test_weights(name, causal):
+    x = make(*SIZES[name], seed=len(name))
+    lse = exact_lse(x, causal)
+    acc = torch.rand(x["kp"].shape[1], x["kp"].shape[0], device=DEV)
+    got = weigh(x, batch_of(x, causal), lse, acc, 0.75)
+    assert_weights(x, got, lse, acc, 0.75, causal)
+
+
+@pytest.mark.parametrize("n_q", [1, 3, 8, 9, 300])
+def test_weights_sum_to_the_queries(n_q):
+    x = make(4, 4, [n_q], [40], 3000)
+    batch = batch_of(x)
+    _, lse = attend(x, batch)
+    got = weigh(x, batch, lse, None, 1.0)
+    # each query's weights sum to 1, up to the errors of its lse (1e-5) and of the sums
+    assert (got.double().sum(1) / n_q - 1).abs().max() < 4e-5
+
+
+def cache(heads, n, seed, ties=False):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    k = torch.randn(n, heads, 64, generator=g, device=DEV).bfloat16()
+    v = torch.randn(n, heads, 64, generator=g, device=DEV).bfloat16()
+    acc = torch.rand(heads, n, generator=g, device=DEV)
+    if ties:
+        acc = (acc * 4).floor() / 4
+    ids = torch.argsort(torch.rand(heads, n, generator=g, device=DEV), 1).int()
+    return k, v, acc, ids
+
+
+def assert_evicted(k, v, acc, ids, keep, recent_from, k2, v2, acc2, ids2):
+    n, heads = k.shape[:2]
+    src = R.evict(acc.cpu(), ids.cpu(), keep, recent_from).to(DEV)
+    h = torch.arange(heads, device=DEV)
+    assert torch.equal(ids2[:, :keep], ids[h[:, None], src])
+    assert torch.equal(acc2[:, :keep].view(torch.int32), acc[h[:, None], src].view(torch.int32))
+    for a, b in ((k, k2), (v, v2)):
+        assert torch.equal(b[:keep].view(torch.int16), a[src.T, h].view(torch.int16))
+        assert torch.equal(b[keep:].view(torch.int16), a[keep:].view(torch.int16))
+
+
+def evict(k, v, acc, ids, keep, recent_from, n=None):
+    n = k.shape[0] if n is None else n
+    k2, v2 = k.clone(), v.clone()
+    acc2, ids2 = torch.full_like(acc, 7.0), torch.full_like(ids, 7)
+    ws = G().new_cache_workspace(k.shape[1], n, keep)
+    G().cache_evict(n, keep, recent_from, k2, v2, acc, ids, acc2, ids2, ws)
+    G().check_device_error(ws)
+    assert (acc2[:, keep:] == 7).all() and (ids2[:, keep:] == 7).all()
+    return k2, v2, acc2, ids2
+
+
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("heads,n,keep", [(1, 1, 1), (2, 2, 1), (1, 31, 7), (3, 33, 32), (2, 257, 256), (16, 1705, 1374),
+                                          (2, 5000, 1), (2, 5000, 4999), (2, 5000, 5000), (4, 8191, 4096), (1, 40000, 20001)])
+def test_evict(heads, n, keep, ties):
+    k, v, acc, ids = cache(heads, n, n + keep, ties)
+    for recent in (0, min(keep, 5), keep, n):
+        assert_evicted(k, v, acc, ids, keep, n - recent, *evict(k, v, acc, ids, keep, n - recent))
+
+
+def test_evict_of_special_values():
+    k, v, acc, ids = cache(2, 3000, 1)
+    inf, nan = float("inf"), float("nan")
+    for i, x in enumerate((inf, -inf, nan, 0.0, -0.0, 1e-45, -1e-45, 3e38, -3e38)):
+        acc[:, i::23] = x
+    for keep in (1, 200, 300, 1500, 2900, 2999):
+        assert_evicted(k, v, acc, ids, keep, 3000, *evict(k, v, acc, ids, keep, 3000))
+    acc[:] = nan
+    assert_evicted(k, v, acc, ids, 1000, 3000, *evict(k, v, acc, ids, 1000, 3000))
+
+
+def test_evict_beyond_shared_memory():
+    # a slice of a head's slots that does not fit a CTA's shared memory
+    k, v, acc, ids = cache(1, 8 * 40 * 1024 + 1000, 5, True)
+    assert_evicted(k, v, acc, ids, 200_000, 400_000, *evict(k, v, acc, ids, 200_000, 400_000))
+
+
+def test_evict_twice_is_evict_once():
+    k, v, acc, ids = cache(2, 3000, 2)
+    k2, v2, acc2, ids2 = evict(k, v, acc, ids, 1700, 2900)
+    assert_evicted(k, v, acc, ids, 1700, 2900, *evict(k2, v2, acc, ids, 1700, 2900))

@@ -64,3 +64,43 @@ def attend(q, kp, vp, ko, vo, q_off, own_off, causal=False, scale=0.125):
             tol_out[rows, h] = (U16 + rel)[:, None] * (p @ v.abs()) * 1.01 + U16 * out[rows, h].abs() * 1.01 + 1e-30
             tol_lse[rows, h] = torch.where(none, torch.zeros_like(z), rel + 8 * U32 * (z.abs() + top))
     return out, lse, tol_out, tol_lse
+
+
+def weights(q, kp, ko, q_off, own_off, lse, acc=None, decay=1.0, causal=False, scale=0.125):
+    """acc_out and the bounds on a kernel's error in it; own tokens of no view are NaN.
+
+    Weight against weight as in attend; the log sum is given, its product with log2(e) and the difference to the
+    score are rounded.
+    """
+    H, Hk, P = q.shape[1], kp.shape[1], kp.shape[0]
+    w = torch.full((Hk, P + ko.shape[0]), float("nan"), dtype=torch.float64, device=q.device)
+    w[:, :P] = 0
+    tol = w.clone()
+    for b, rows, cols in views(q_off, own_off):
+        own = slice(P + cols.start, P + cols.stop)
+        w[:, own], tol[:, own] = 0, 0
+        for h in range(H):
+            hk = h // (H // Hk)
+            s, size = scores(q, kp, ko, rows, cols, h, hk, causal, scale)
+            z = lse[rows, h].double()[:, None]
+            p = torch.where((z == NEG) | (s == NEG), torch.zeros_like(s), (s - z).exp())
+            rel = 130 * U32 * size + 4e-6 + 4 * U32 * (z.abs() + s.abs().nan_to_num(0, 0, 0) + 64) + (q.shape[0] * (H // Hk) / 64 + 64) * U32
+            rel = torch.where(p > 0, rel, torch.zeros_like(rel))
+            for at, cut in ((slice(0, P), slice(0, P)), (own, slice(P, None))):
+                w[hk, at] += p[:, cut].sum(0)
+                tol[hk, at] += (p * rel)[:, cut].sum(0) * 1.01
+    if acc is not None and decay:
+        w[:, :P] += decay * acc[:, :P].double()
+        tol[:, :P] += 4 * U32 * (w[:, :P].abs() + decay * acc[:, :P].double().abs())
+    return w, tol + 1e-30
+
+
+def evict(acc, ids, keep, recent_from):
+    """source[h][slot]: the slot whose token ends up in `slot`, for slots below `keep`."""
+    out = []
+    for a, i in zip(acc.double().tolist(), ids.tolist()):
+        key = [float("inf") if t >= recent_from else (NEG if x != x else x) for x, t in zip(a, i)]
+        kept = set(sorted(range(len(key)), key=lambda s: (-key[s], s))[:keep])
+        movers = iter(sorted(s for s in kept if s >= keep))
+        out.append([s if s in kept else next(movers) for s in range(keep)])
+    return torch.tensor(out, dtype=torch.int64).reshape(len(out), keep)
