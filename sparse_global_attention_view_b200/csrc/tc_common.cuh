@@ -271,6 +271,15 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
                : "memory");
 }
 
+// Is this the lane that issues for its (converged) warp?  Code that all lanes run
+// with only the tcgen05 instructions behind this keeps descriptors and addresses
+// in uniform registers; under `lane == 0` each instruction moves them there first.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
+}
+
 // ---------------------------------------------------------------------------
 // softmax arithmetic
 

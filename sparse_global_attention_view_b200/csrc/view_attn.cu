@@ -9,20 +9,21 @@
 //
 // view_attn_kernel (tcgen05 / TMEM / TMA): one CTA = up to two 128-row query
 // tiles of one key head.  A row is a (token, query head of the group) pair, so
-// the G query heads that share a key head share its K/V tiles.  12 warps:
+// the G query heads that share a key head share its K/V tiles.  20 warps:
 //   warp 0      TMA producer: the Q tiles once, then a 6-stage ring of 128-key K/V
 //               tiles; zeroes the value rows behind a view's last key;
-//   warps 1, 3  MMA issuers, one for each tile: S = Q K^T into TMEM, O += P V with P from TMEM;
+//   warps 1, 3  MMA issuers of two streams each;
 //   warp 2      TMEM allocation;
-//   warps 4-11  softmax, one warpgroup a tile, one thread a row.
-// The softmax takes a score tile into registers and hands S back at once, and P
-// has columns of its own (S 2 x 128, O 2 x 64, P 2 x 64 of the 512), so the next
-// Q K^T runs while the exponentials of the present tile are taken; a warp never
-// waits for a product in the steady state.  Bound by the exponentials and the
-// instructions around them (two per 128 flops at a head width of 64).
-// With at most 128 rows the two slots take alternate key tiles of the same
-// rows instead; their results count as separate partial results.
-//
+//   warps 4-19  softmax, one warpgroup a stream, one thread a row.
+// A stream is one query tile against one 64-key half of every key tile: it has a
+// softmax state, 64 TMEM columns of scores (P is written over them) and 64 of
+// output of its own.  Two streams serve a query tile; with one tile of rows all
+// four do, each with half of every other key tile.  Streams never wait for one
+// another; their results are joined in shared memory at the end.  Four streams
+// give every scheduler four softmax warps: a step of one of them (load, maximum,
+// exponentials, store, two products) is a chain of latencies that only other
+// warps can fill, and with two tiles of 128 x 128 scores and two warps a
+// scheduler the exponential units idled half the time.
 // view_own_kernel: views of few rows.  Their own keys are read by CUDA cores
 // (eight lanes a key, plain 16-byte loads: nothing is read that no query sees),
 // and the partial results against the prefix are merged in the same pass.
@@ -44,30 +45,34 @@ using namespace tc;
 
 constexpr int kPolyOf8 = 2;  // pairs of exponentials in eight on the FMA pipe
 constexpr int TK = 128;      // keys per key tile
+constexpr int HK = 64;       // keys of a stream's half
+constexpr int NS = 4;        // streams
 constexpr int ST = 6;        // K/V ring stages
-constexpr int kThreads = 384;
+constexpr int kThreads = 128 + 128 * NS;
 constexpr uint32_t kTile = 128 * 128;  // bytes of one [128][64] bf16 tile
 
 constexpr uint32_t OFF_Q = 0;
 constexpr uint32_t OFF_K = OFF_Q + 2 * kTile;
 constexpr uint32_t OFF_V = OFF_K + ST * kTile;
 constexpr uint32_t OFF_BAR = OFF_V + ST * kTile;
-constexpr uint32_t OFF_MISC = OFF_BAR + 256;
+constexpr uint32_t OFF_MISC = OFF_BAR + 384;
 constexpr uint32_t kSmemBytes = OFF_MISC + 64 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+// results on their way to another stream: 64 values, maximum and sum a row, over the ring
+constexpr int JOIN = 67;  // odd: a thread a row without bank conflicts
+static_assert((NS - 1) * 128 * JOIN * 4 <= 2 * ST * kTile, "join area");
 
-constexpr int B_Q = 0, B_KF = 1, B_VF = B_KF + ST, B_KVE = B_VF + ST, B_SF = B_KVE + ST, B_SE = B_SF + 2,
-              B_PF = B_SE + 2, B_PE = B_PF + 2, B_VZ = B_PE + 2, B_DRAIN = B_VZ + 1, B_COUNT = B_DRAIN + 2;
-static_assert(B_COUNT * 8 <= 256, "barrier area");
+constexpr int B_Q = 0, B_KF = 1, B_VF = B_KF + ST, B_KVE = B_VF + ST, B_SF = B_KVE + ST, B_PF = B_SF + NS,
+              B_OF = B_PF + NS, B_VZ = B_OF + NS, B_END = B_VZ + 1, B_JOIN = B_END + 1, B_DRAIN = B_JOIN + 1,
+              B_COUNT = B_DRAIN + 2;
+static_assert(B_COUNT * 8 <= 384, "barrier area");
 
-constexpr uint32_t kCols = 512, COL_O = 256, COL_P = 384;  // TMEM: S_t at 128 t, O_t, P_t at 64 t behind
-constexpr int kLaunchRegs = 168, kRegsLow = 72, kRegsHigh = 216;
-static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kLaunchRegs, "register split");
+constexpr uint32_t kCols = 512, COL_O = 256;  // TMEM: stream x has S, then P, at 64 x, and O at 256 + 64 x
 
 struct ViewAttnArgs {
   ViewDims d;
   int rows_tok;   // tokens per row tile: 128 / G
-  int aligned, do_prefix, do_own, pair, check_views;
+  int aligned, do_prefix, do_own, check_views;
   int n_split, units_per_view;
   bf16* out;      // written directly when part_o is null
   float* lse;     // nullable
@@ -99,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.y;
   const int unit = blockIdx.x / a.n_split, split = blockIdx.x - unit * a.n_split;
-  const int MT = a.rows_tok, unit_tok = a.pair ? MT : 2 * MT;
+  const int MT = a.rows_tok, unit_tok = 2 * MT;
 
   // this CTA's rows [tok0, tok_end) and keys; uniform over the CTA
   long long tok0;
@@ -129,9 +134,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nt_all = np + (nk_seen + TK - 1) / TK;
   const int j0 = (int)((long long)nt_all * split / a.n_split);
   const int nt = (int)((long long)nt_all * (split + 1) / a.n_split) - j0;
-  // steps of slot t: its i-th one is key tile j0 + i, or j0 + 2 i + t
-  const int active = a.pair ? 2 : (tok0 + MT < tok_end ? 2 : 1);
-  auto steps = [&](int t) -> int { return t >= active ? 0 : (a.pair ? (nt + 1 - t) / 2 : nt); };
+  // one tile of rows: issuer w and its streams take every other key tile, else
+  // all key tiles of query tile w.  The i-th step is key tile j0 + at(w, i)
+  const bool one = tok0 + MT >= tok_end;
+  auto at = [&](int w, int i) -> int { return one ? 2 * i + w : i; };
+  auto steps = [&](int w) -> int { return one ? (nt + 1 - w) / 2 : nt; };
   // the value rows behind the view's last seen key hold other tokens: zeroed
   const bool zero_tail = nt > 0 && j0 + nt == nt_all && nt_all > np && (nk_seen % TK) != 0;
 
@@ -140,16 +147,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < ST; ++s) {
       mbar_init(bar(B_KF + s), 1);
       mbar_init(bar(B_VF + s), 1);
-      mbar_init(bar(B_KVE + s), a.pair ? 1 : active);
+      mbar_init(bar(B_KVE + s), one ? 1 : 2);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(B_SF + t), 1);
-      mbar_init(bar(B_SE + t), 4);
-      mbar_init(bar(B_PF + t), 4);
-      mbar_init(bar(B_PE + t), 1);
-      mbar_init(bar(B_DRAIN + t), 1);
+    for (int x = 0; x < NS; ++x) {
+      mbar_init(bar(B_SF + x), 1);
+      mbar_init(bar(B_PF + x), 4);
+      mbar_init(bar(B_OF + x), 1);
     }
     mbar_init(bar(B_VZ), 1);
+    mbar_init(bar(B_END), 4 * NS);
+    mbar_init(bar(B_JOIN), 4 * NS);
+    mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_DRAIN + 1), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -163,11 +172,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tbase = *tmem_slot;
   const long long limit = d.wait_cycles;
 
-  if (warp < 4) regs_dec<kRegsLow>();
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (lane == 0 && nt > 0) {
-      const int q_tiles = a.pair ? 1 : active;
+      const int q_tiles = one ? 1 : 2;
       mbar_expect_tx(bar(B_Q), (uint32_t)(q_tiles * MT * d.G) * 128u);
       for (int t = 0; t < q_tiles; ++t) tma_load_3d(sQ + t * kTile, &tq, bar(B_Q), 0, hk * d.G, (int)(tok0 + t * MT));
       int issued = 0;
@@ -207,53 +215,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1 || warp == 3) {
-    // ---------------- MMA issuer of slot t ----------------
-    const int t = warp >> 1;
-    const int n = steps(t);
-    if (lane == 0 && n > 0) {
-      const uint32_t id_qk = idesc(128, 128, kFmtBF16, 0, 0);
+    // ---------------- MMA issuer of streams 2 w and 2 w + 1 ----------------
+    // the whole warp runs the loop, one lane issues
+    const int w = __shfl_sync(0xffffffffu, warp >> 1, 0), n = steps(w);
+    if (n > 0) {
+      const bool leader = elect_one();
+      const uint32_t id_qk = idesc(128, HK, kFmtBF16, 0, 0);
       const uint32_t id_pv = idesc(128, 64, kFmtBF16, 0, 1);
-      const uint32_t q_tile = sQ + (a.pair ? 0 : t) * kTile;
-      auto at = [&](int i) -> int { return a.pair ? 2 * i + t : i; };  // ring index of step i
-      auto issue_s = [&](int i) {
-        const uint32_t k_tile = sK + (at(i) % ST) * kTile;
+      const uint64_t q_desc = sdesc_k(sQ + (one ? 0 : w) * kTile);
+      const uint64_t k_desc = sdesc_k(sK), v_desc = sdesc_mn(sV);
+      auto wait = [&](int b, uint32_t parity) { return warp_wait(bar(b), parity, abort_flag, a.err, limit); };
+      // descriptors count 16-byte units
+      auto issue_s = [&](int s, int half) {
+        const uint32_t x = 2 * w + half;
+        const uint64_t kd = k_desc + (uint64_t)(s * (kTile >> 4) + half * (HK * 128 >> 4));
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_bf16_ss(tbase + t * 128, sdesc_k(q_tile + kk * 32), sdesc_k(k_tile + kk * 32), id_qk, kk > 0);
-        mma_commit(bar(B_SF + t));
+          for (int kk = 0; kk < 4; ++kk) mma_bf16_ss(tbase + x * 64, q_desc + kk * 2, kd + kk * 2, id_qk, kk > 0);
+          mma_commit(bar(B_SF + x));
+        }
       };
-      auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity, abort_flag, a.err, limit); };
-      auto k_full = [&](int i) { return wait(B_KF + at(i) % ST, (at(i) / ST) & 1); };
-      bool ok = wait(B_Q, 0) && k_full(0);
+      // ring stage and phase of the present and the next step
+      const int step = one ? 2 : 1;
+      int s = one ? w : 0, s1 = s;
+      uint32_t ph = 0, ph1 = 0;
+      bool ok = wait(B_Q, 0) && wait(B_KF + s, 0);
       if (ok) {
         fence_after_sync();
-        issue_s(0);
+        issue_s(s, 0);
+        issue_s(s, 1);
       }
       for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n) {
-          ok = k_full(i + 1) && wait(B_SE + t, i & 1);
+        s1 = s + step;
+        ph1 = ph;
+        if (s1 >= ST) {
+          s1 -= ST;
+          ph1 ^= 1;
+        }
+        ok = wait(B_VF + s, ph);
+        if (ok && zero_tail && at(w, i) == nt - 1) ok = wait(B_VZ, 0);
+        if (ok && i + 1 < n) ok = wait(B_KF + s1, ph1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t x = 2 * w + half;
+          if (ok) ok = wait(B_PF + x, i & 1);
           if (!ok) break;
           fence_after_sync();
-          issue_s(i + 1);
-        }
-        const int s = at(i) % ST;
-        ok = wait(B_VF + s, (at(i) / ST) & 1);
-        if (ok && zero_tail && at(i) == nt - 1) ok = wait(B_VZ, 0);
-        ok = ok && wait(B_PF + t, i & 1);
-        if (!ok) break;
-        fence_after_sync();
+          const uint64_t vd = v_desc + (uint64_t)(s * (kTile >> 4) + half * (HK * 128 >> 4));
+          if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ts(tbase + COL_O + t * 64, tbase + COL_P + t * 64 + kk * 8, sdesc_mn(sV + s * kTile + kk * 2048),
-                      id_pv, (i > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(bar(B_PE + t));
-        mma_commit(bar(B_KVE + s));
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ts(tbase + COL_O + x * 64, tbase + x * 64 + kk * 8, vd + kk * (2048 >> 4), id_pv,
+                          (i > 0 || kk > 0) ? 1u : 0u);
+          }
+          if (i + 1 < n) {
+            // the scores come over the P just read: products complete in order
+            issue_s(s1, half);
+          } else if (leader) {
+            mma_commit(bar(B_OF + x));
+          }
+        }
+        if (ok && leader) mma_commit(bar(B_KVE + s));
+        s = s1;
+        ph = ph1;
       }
       if (!ok) {
         // wait for the products already issued before TMEM is released
         volatile int never = 0;
-        mma_commit(bar(B_DRAIN + t));
-        mbar_wait(bar(B_DRAIN + t), 0, &never, a.err);
+        if (leader) mma_commit(bar(B_DRAIN + w));
+        __syncwarp();
+        mbar_wait(bar(B_DRAIN + w), 0, &never, a.err);
       }
     }
   } else if (warp == 2) {
@@ -262,126 +293,102 @@ __global__ void __launch_bounds__(kThreads, 1)
       ViewRange r;
       for (int b = lane; b < d.B; b += 32) view_range(d, b, &r, a.err);
     }
-  } else {
-    regs_inc<kRegsHigh>();
-    // ---------------- softmax, one thread a row ----------------
-    const int t = (warp - 4) >> 2;
+  } else if (warp >= 4) {
+    // ---------------- softmax of stream x, one thread a row ----------------
+    const int x = (warp - 4) >> 2, w = x >> 1, half = x & 1;
     const int row = (warp & 3) * 32 + lane;
     const int tl = row / d.G, g = row - tl * d.G;
-    const long long tok = tok0 + (a.pair ? 0 : t * MT) + tl;
-    const bool valid = t < active && tl < MT && tok >= tok_lo && tok < tok_end;
+    const long long tok = tok0 + (one ? 0 : w * MT) + tl;
+    const bool valid = tl < MT && tok >= tok_lo && tok < tok_end;
     // own keys [0, own_end) of the view are seen by this row
     int own_end = nk;
     if (d.causal && valid) own_end = max(0, min(nk, (int)(tok - q0) + nk - nq + 1));
     const bool work = __any_sync(0xffffffffu, valid);
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tbase + lane_off + t * 128;
-    const uint32_t o_addr = tbase + lane_off + COL_O + t * 64;
-    const uint32_t p_addr = tbase + lane_off + COL_P + t * 64;
+    const uint32_t s_addr = tbase + ((uint32_t)((warp & 3) * 32) << 16) + x * 64;
+    const uint32_t o_addr = s_addr + COL_O;
     const float c2 = d.c2;
-    const int n = steps(t);
+    const int n = steps(w);
     float m_used = -CUDART_INF_F, l = 0.f;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      ok = warp_wait(bar(B_SF + t), i & 1, abort_flag, a.err, limit);
+      // S of this step, and with it the product of the step before, is complete
+      ok = warp_wait(bar(B_SF + x), i & 1, abort_flag, a.err, limit);
       if (!ok) break;
       fence_after_sync();
-      if (!work) {
-        // no rows: only the barriers, in step with the other warps
-        if (lane == 0) mbar_arrive(bar(B_SE + t));
-        if (i > 0) ok = warp_wait(bar(B_PE + t), (i - 1) & 1, abort_flag, a.err, limit);
-        if (!ok) break;
-        fence_before_sync();
-        if (lane == 0) mbar_arrive(bar(B_PF + t));
-        continue;
-      }
-      uint32_t sv[4][32];
+      if (work) {
+        uint32_t sv[2][32];
+        tmem_ld32(s_addr, sv[0]);
+        tmem_ld32(s_addr + 32, sv[1]);
+        tmem_wait_ld();
+        const int j = j0 + at(w, i);
+        const int end = (j < np ? d.n_prefix - j * TK : own_end - (j - np) * TK) - half * HK;
+        if (end < HK) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, sv[c]);
-      tmem_wait_ld();
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_SE + t));
-      const int j = j0 + (a.pair ? 2 * i + t : i);
-      const int end = j < np ? d.n_prefix - j * TK : own_end - (j - np) * TK;
-      if (end < TK) {
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+            for (int u = 0; u < 32; ++u)
+              if (32 * c + u >= end) sv[c][u] = __float_as_uint(-CUDART_INF_F);
+        }
+        // eight independent chains: a thread owns a whole row
+        auto sval = [&](int k) -> float { return __uint_as_float(sv[k >> 5][k & 31]); };
+        float mq[8];
 #pragma unroll
-          for (int u = 0; u < 32; ++u)
-            if (32 * c + u >= end) sv[c][u] = __float_as_uint(-CUDART_INF_F);
-      }
-      // eight independent chains: a thread owns a whole row
-      auto sval = [&](int k) -> float { return __uint_as_float(sv[k >> 5][k & 31]); };
-      float mq[8];
+        for (int u = 0; u < 8; ++u) mq[u] = max_nan(sval(u), sval(u + 8));
 #pragma unroll
-      for (int u = 0; u < 8; ++u) mq[u] = max_nan(sval(u), sval(u + 8));
+        for (int k = 16; k < HK; k += 16)
 #pragma unroll
-      for (int k = 16; k < 128; k += 16)
+          for (int u = 0; u < 8; ++u) mq[u] = max3_nan(mq[u], sval(k + u), sval(k + 8 + u));
+        const float mx = max3_nan(max3_nan(mq[0], mq[1], mq[2]), max3_nan(mq[3], mq[4], mq[5]), max_nan(mq[6], mq[7]));
+        float mxs = mx * c2;
+        if (mxs == CUDART_INF_F) mxs = CUDART_NAN_F;  // infinity - infinity
+        // the maximum in use is raised only when a score exceeds it by 2^8; a NaN
+        // score makes it NaN, and with it the row
+        const bool need = !(mxs <= m_used + 8.f);
+        if (__any_sync(0xffffffffu, need)) {
+          const float corr = need ? exp2f(m_used - mxs) : 1.f;
+          if (i > 0) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) mq[u] = max3_nan(mq[u], sval(k + u), sval(k + 8 + u));
-      const float mx = max3_nan(max3_nan(mq[0], mq[1], mq[2]), max3_nan(mq[3], mq[4], mq[5]), max_nan(mq[6], mq[7]));
-      float mxs = mx * c2;
-      if (mxs == CUDART_INF_F) mxs = CUDART_NAN_F;  // infinity - infinity
-      // the maximum in use is raised only when a score exceeds it by 2^8; a NaN
-      // score makes it NaN, and with it the row
-      const bool need = !(mxs <= m_used + 8.f);
-      if (__any_sync(0xffffffffu, need)) {
-        const float corr = need ? exp2f(m_used - mxs) : 1.f;
-        if (i > 0) {
-          ok = warp_wait(bar(B_PE + t), (i - 1) & 1, abort_flag, a.err, limit);
-          if (!ok) break;
-          fence_after_sync();
+            for (int c = 0; c < 4; ++c) {
+              uint32_t ov[16];
+              tmem_ld16(o_addr + 16 * c, ov);
+              tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t ov[16];
-            tmem_ld16(o_addr + 16 * c, ov);
-            tmem_wait_ld();
-#pragma unroll
-            for (int u = 0; u < 16; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * corr);
-            tmem_st16(o_addr + 16 * c, ov);
+              for (int u = 0; u < 16; ++u) ov[u] = __float_as_uint(__uint_as_float(ov[u]) * corr);
+              tmem_st16(o_addr + 16 * c, ov);
+            }
+          }
+          if (need) {
+            l *= corr;
+            m_used = mxs;
           }
         }
-        if (need) {
-          l *= corr;
-          m_used = mxs;
-        }
-      }
-      // a row that has seen no key yet keeps finite arithmetic: weights 2^-inf = 0
-      const float shift = m_used == -CUDART_INF_F ? 0.f : -m_used;
-      const uint64_t c2p = f2_pack(c2, c2), nmp = f2_pack(shift, shift);
-      uint64_t ps2[4] = {0ull, 0ull, 0ull, 0ull};
+        // a row that has seen no key yet keeps finite arithmetic: weights 2^-inf = 0
+        const float shift = m_used == -CUDART_INF_F ? 0.f : -m_used;
+        const uint64_t c2p = f2_pack(c2, c2), nmp = f2_pack(shift, shift);
+        uint64_t ps2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const uint64_t x2 =
-              f2_fma(f2_pack(__uint_as_float(sv[c][2 * u]), __uint_as_float(sv[c][2 * u + 1])), c2p, nmp);
-          uint64_t p2;
-          if ((u & 7) >= 8 - kPolyOf8) {
-            p2 = exp2_poly2(x2);
-          } else {
-            float x0, x1;
-            f2_unpack(x2, x0, x1);
-            p2 = f2_pack(exp2_mufu(x0), exp2_mufu(x1));
+          for (int u = 0; u < 16; ++u) {
+            const uint64_t x2 =
+                f2_fma(f2_pack(__uint_as_float(sv[c][2 * u]), __uint_as_float(sv[c][2 * u + 1])), c2p, nmp);
+            uint64_t p2;
+            if ((u & 7) >= 8 - kPolyOf8) {
+              p2 = exp2_poly2(x2);
+            } else {
+              float x0, x1;
+              f2_unpack(x2, x0, x1);
+              p2 = f2_pack(exp2_mufu(x0), exp2_mufu(x1));
+            }
+            ps2[u & 3] = f2_add(ps2[u & 3], p2);
+            float p0, p1;
+            f2_unpack(p2, p0, p1);
+            pk[u] = pack_bf16x2(p0, p1);
           }
-          ps2[u & 3] = f2_add(ps2[u & 3], p2);
-          float p0, p1;
-          f2_unpack(p2, p0, p1);
-          pk[u] = pack_bf16x2(p0, p1);
+          tmem_st16(s_addr + 16 * c, pk);
         }
-        // P of the step before has to be read before it is written over
-        if (c == 0 && i > 0) {
-          ok = warp_wait(bar(B_PE + t), (i - 1) & 1, abort_flag, a.err, limit);
-          if (!ok) break;
-          fence_after_sync();
-        }
-        tmem_st16(p_addr + 16 * c, pk);
-      }
-      if (!ok) break;
-      tmem_wait_st();
-      {
+        tmem_wait_st();
         const uint64_t s01 = f2_add(f2_add(ps2[0], ps2[1]), f2_add(ps2[2], ps2[3]));
         float lo, hi;
         f2_unpack(s01, lo, hi);
@@ -389,41 +396,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_PF + t));
+      if (lane == 0) mbar_arrive(bar(B_PF + x));
     }
-    if (ok && n > 0) ok = warp_wait(bar(B_PE + t), (n - 1) & 1, abort_flag, a.err, limit);
-    if (ok && work) {
+    if (ok && n > 0) ok = warp_wait(bar(B_OF + x), 0, abort_flag, a.err, limit);
+    // all streams are through with the ring: their results meet there
+    if (ok) {
       fence_after_sync();
-      // no key seen: zeros and a log sum of -infinity (a NaN score left l NaN)
-      const bool empty = m_used == -CUDART_INF_F && !(l != l);
-      const float inv = empty ? 0.f : 1.f / l;
-      const float lse2 = empty ? -CUDART_INF_F : m_used + log2f(l);
+      if (lane == 0) mbar_arrive(bar(B_END));
+      ok = warp_wait(bar(B_END), 0, abort_flag, a.err, limit);
+    }
+    // slot of the join area; the first stream of a tile collects
+    const int slot = one ? x - 1 : (half ? w : -1);
+    float* join = reinterpret_cast<float*>(sp + OFF_K) + row * JOIN;
+    if (ok && slot >= 0) {
+      float* mine = join + slot * 128 * JOIN;
+      mine[64] = m_used;
+      mine[65] = l;
+      if (n > 0 && work) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t ov[16];
+          tmem_ld16(o_addr + 16 * c, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 16; ++u) mine[16 * c + u] = __uint_as_float(ov[u]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_JOIN));
+    } else if (ok) {
+      if (lane == 0) mbar_arrive(bar(B_JOIN));
+      ok = warp_wait(bar(B_JOIN), 0, abort_flag, a.err, limit);
+    }
+    if (ok && slot < 0 && work) {
+      // (maximum, sum, values) of the streams that share the rows
+      const int first = one ? 0 : w, others = one ? NS - 1 : 1;
+      float m = m_used;
+      for (int k = 0; k < others; ++k) m = fmaxf(m, join[(first + k) * 128 * JOIN + 64]);
+      // 2^(m_k - m): 0 for a stream that saw no key, NaN for one that saw a NaN
+      auto factor = [&](float mk) -> float { return mk == -CUDART_INF_F ? 0.f : exp2f(mk - m); };
+      const float f0 = factor(m_used);
+      float lt = m_used == -CUDART_INF_F ? l * 0.f : l * f0;
+      for (int k = 0; k < others; ++k) {
+        const float* o = join + (first + k) * 128 * JOIN;
+        lt += o[64] == -CUDART_INF_F ? o[65] * 0.f : o[65] * factor(o[64]);
+      }
+      // no key seen: zeros and a log sum of -infinity
+      const bool empty = lt == 0.f;
+      const float inv = empty ? 0.f : 1.f / lt;
+      const float lse2 = empty ? -CUDART_INF_F : m + log2f(lt);
       const int h = hk * d.G + g;
       const long long rh = tok * d.H + h;
-      const long long part = a.part0 + (a.pair ? 2 * split + t : split);
+      const long long part = a.part0 + split;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
+        float o[16];
         uint32_t ov[16];
         if (n > 0) {
           tmem_ld16(o_addr + 16 * c, ov);
           tmem_wait_ld();
         }
         if (!valid) continue;
-        float o[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u) o[u] = empty ? 0.f : __uint_as_float(ov[u]) * inv;
+        for (int u = 0; u < 16; ++u) o[u] = f0 == 0.f ? 0.f : __uint_as_float(ov[u]) * f0;
+        for (int k = 0; k < others; ++k) {
+          const float* src = join + (first + k) * 128 * JOIN;
+          const float f = factor(src[64]);
+          if (f == 0.f) continue;  // nothing was stored where no key was seen
+#pragma unroll
+          for (int u = 0; u < 16; ++u) o[u] = fmaf(src[16 * c + u], f, o[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 16; ++u) o[u] *= inv;
         if (a.part_o) {
           if (empty) continue;  // the merge skips it by its log sum
           float4* dst = reinterpret_cast<float4*>(a.part_o + ((part * d.n_q * d.H + rh) * 64 + 16 * c));
 #pragma unroll
           for (int u = 0; u < 4; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
         } else {
-          uint32_t w[8];
+          uint32_t pw[8];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) w[u] = pack_bf16x2(o[2 * u], o[2 * u + 1]);
+          for (int u = 0; u < 8; ++u) pw[u] = pack_bf16x2(o[2 * u], o[2 * u + 1]);
           uint4* dst = reinterpret_cast<uint4*>(a.out + tok * d.o_stride + h * 64 + 16 * c);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          dst[0] = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+          dst[1] = make_uint4(pw[4], pw[5], pw[6], pw[7]);
         }
       }
       if (valid) {
@@ -638,13 +694,7 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
 // host
 
 cudaError_t prepare_kernel() {
-  cudaError_t e = cudaFuncSetAttribute(view_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-  if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, view_attn_kernel);
-  if (e != cudaSuccess) return e;
-  // the register split waits forever on another launch allocation
-  return fa.numRegs == kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(view_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
 }
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
@@ -686,19 +736,17 @@ ViewPlan view_plan(const ViewDims& d) {
   // partial results of one launch of a kind: their bytes against a key tile's time
   const double merge = 1.0 + (double)d.n_q * d.H * 64 * 8 / 3.0e6;
   if (p.packed) {
-    p.pair_packed = d.n_q <= MT;
-    const long long units = (long long)ceil_div(d.n_q, p.pair_packed ? MT : 2 * MT) * d.Hk;
+    const long long units = (long long)ceil_div(d.n_q, 2 * MT) * d.Hk;
     p.split_packed = choose_split(units, np, 64, 4.0, merge);
-    p.parts += p.split_packed * (p.pair_packed ? 2 : 1);
+    p.parts += p.split_packed;
   }
   if (p.aligned) {
-    p.pair_aligned = d.max_q <= MT;
-    const int unit_tok = p.pair_aligned ? MT : 2 * MT;
+    const int unit_tok = 2 * MT;
     long long units = (long long)d.B * ceil_div(d.max_q, unit_tok);
     const long long bound = d.n_q / unit_tok + d.B;  // rows there are, and a ragged end a view
     if (units > bound) units = bound;
     p.split_aligned = choose_split(units * d.Hk, (p.aligned_prefix ? np : 0) + no, 64, 4.0, merge);
-    p.parts += p.split_aligned * (p.pair_aligned ? 2 : 1);
+    p.parts += p.split_aligned;
   }
   // one part that nothing else joins is the result
   if (p.parts == 1 && !p.small_own) p.parts = 0;
@@ -740,23 +788,21 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
       a.do_prefix = 1;
       a.do_own = 0;
       a.check_views = !p.aligned && !p.small_own;
-      a.pair = p.pair_packed;
       a.n_split = p.split_packed;
       a.units_per_view = 0;
       a.part0 = 0;
-      const dim3 grid((unsigned)(ceil_div(d.n_q, a.pair ? MT : 2 * MT) * a.n_split), (unsigned)d.Hk);
+      const dim3 grid((unsigned)(ceil_div(d.n_q, 2 * MT) * a.n_split), (unsigned)d.Hk);
       view_attn_kernel<<<grid, kThreads, kSmemBytes, st>>>(mq, mkp, mvp, mko, mvo, a);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
-      a.part0 = p.split_packed * (p.pair_packed ? 2 : 1);
+      a.part0 = p.split_packed;
     }
     if (p.aligned) {
       a.aligned = 1;
       a.do_prefix = p.aligned_prefix;
       a.do_own = p.aligned_own;
-      a.pair = p.pair_aligned;
       a.n_split = p.split_aligned;
-      a.units_per_view = ceil_div(d.max_q, a.pair ? MT : 2 * MT);
+      a.units_per_view = ceil_div(d.max_q, 2 * MT);
       const dim3 grid((unsigned)(d.B * a.units_per_view * a.n_split), (unsigned)d.Hk);
       view_attn_kernel<<<grid, kThreads, kSmemBytes, st>>>(mq, mkp, mvp, mko, mvo, a);
       e = cudaGetLastError();

@@ -26,7 +26,6 @@ struct ViewPlan {
   // alone, rows aligned to views against both, or against their own keys alone
   int packed, aligned, aligned_prefix, aligned_own;
   int small_own;   // the views' own keys by the CUDA-core kernel, which also merges
-  int pair_packed, pair_aligned;  // one row tile a CTA, its two slots taking alternate key tiles
   int split_packed, split_aligned;  // key splits
   int parts;       // partial results per (query, head); 0: written directly
 };
