@@ -8,13 +8,20 @@
 // as sources lie behind n_keep and targets before it, moves need no order and
 // the call may be repeated.
 //
-// select_kernel: one cluster of CTAs a head, each with a slice of the slots, its
-// sort keys in shared memory (read again from memory where a slice does not
-// fit).  A radix selection finds the n_keep-th key in three passes of 11, 11 and
-// 10 bits, with histograms in shared memory that the CTAs read from one another;
-// then the counts of equal keys, of free slots and of movers before every warp's
-// part of the slots give each its rank.  Integer arithmetic throughout, so the
-// result depends on the inputs alone.  Bound by the latency of its passes.
+// select_kernel: a cluster of eight CTAs a head (one for few slots), each with a
+// slice of the slots and the leading halves of their sort keys in shared memory
+// (16 bits tell almost all keys apart; the others, and slices that do not fit, are
+// read again).  A radix selection finds the n_keep-th key in three passes of 11,
+// 11 and 10 bits: the CTAs add their counts of each digit to one another's shared
+// memory, one barrier a pass.  Then the counts of equal keys, of free slots and of
+// movers before every thread's part of the slots give each its rank.  Integer
+// arithmetic throughout, so the result depends on the inputs alone.  Bound by
+// instruction issue and latency, not by its bytes: counting takes the slots thread
+// by thread with a run of equal digits held in a register (a cache of equal
+// accounts would queue up at one counter), ranking gives every thread an odd
+// number of consecutive slots (no votes, one scan of the block).  CTAs behind the
+// clusters' copy the accounts and numbers of all slots below n_keep meanwhile;
+// the movers' come over those of the free slots afterwards.
 // move_kernel: copies K and V rows, eight lanes a row.  Bound by memory.
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -26,17 +33,18 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int CLUSTER = 8;
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int BINS = 2048;
-constexpr int kMaxKeys = 40 * 1024;  // sort keys of a slice in shared memory
+constexpr int kFewSlots = 8192;       // one CTA a head: 9 us against 14 of a cluster at 1705 slots
+constexpr int kMaxKeys = 96 * 1024;   // sort keys of a slice in shared memory, two bytes each
+constexpr int kCopyCtas = 64;
 
 struct Shared {
-  uint32_t hist[BINS];
+  uint32_t counts[BINS];   // this CTA's
+  uint32_t sums[2][BINS];  // the cluster's, one pass in use while the other is cleared
   uint32_t warp_sum[kWarps];
-  uint32_t tot[4];        // this CTA's counts, read by the others
-  uint32_t bin, above;    // the bin that holds the wanted key; keys above it
-  uint32_t before[kWarps][2];
+  uint32_t tot[4];         // this CTA's counts, read by the others
+  uint32_t bin, above;     // the bin that holds the wanted key; keys above it
 };
 
 // Larger account, larger key; NaN counts as -infinity and -0 as 0.
@@ -60,41 +68,75 @@ struct EvictArgs {
   int* dst;      // [Hk][most]
 };
 
-// Exclusive sum over the warps of the block of a value that lane 0 holds.
-__device__ __forceinline__ uint32_t warps_before(uint32_t v, uint32_t* scratch, uint32_t* total) {
+// Exclusive sum over the threads of the block.
+__device__ __forceinline__ uint32_t threads_before(uint32_t v, uint32_t* scratch, uint32_t* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();
-  if (lane == 0) scratch[warp] = v;
-  __syncthreads();
-  uint32_t x = scratch[lane], sum = x;  // 32 warps
+  uint32_t sum = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += y;
   }
-  *total = __shfl_sync(0xffffffffu, sum, 31);
-  return __shfl_sync(0xffffffffu, sum - x, warp);
+  __syncthreads();
+  if (lane == 31) scratch[warp] = sum;
+  __syncthreads();
+  uint32_t w = scratch[lane];  // 32 warps
+  const uint32_t own = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  return __shfl_sync(0xffffffffu, w - own, warp) + sum - v;
 }
 
-template <bool IN_SMEM>
-__global__ void __launch_bounds__(kThreads, 1) select_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t s_keys[];
+template <int CLUSTER, bool IN_SMEM>
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a) {
+  extern __shared__ uint16_t s_top[];
   __shared__ Shared sh;
+  const int tid = threadIdx.x;
+  pdl_launch();
+  if ((int)blockIdx.x >= a.Hk * CLUSTER) {
+    // whole clusters of copying CTAs
+    const int step = (int)(gridDim.x - a.Hk * CLUSTER) * kThreads, first = (int)(blockIdx.x - a.Hk * CLUSTER) * kThreads + tid;
+    for (int h = 0; h < a.Hk; ++h) {
+      const long long row = h * a.w_stride;
+#pragma unroll 2
+      for (int i = first; i < a.keep; i += step) {
+        a.acc_out[row + i] = a.acc[row + i];
+        a.ids_out[row + i] = a.ids[row + i];
+      }
+    }
+    return;
+  }
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), hk = blockIdx.x / CLUSTER;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto sync_all = [&]() {
+    if (CLUSTER > 1)
+      cluster.sync();
+    else
+      __syncthreads();
+  };
+  auto of_rank = [&](uint32_t* p, int r) -> uint32_t* { return CLUSTER > 1 ? cluster.map_shared_rank(p, r) : p; };
+  const int rank = CLUSTER > 1 ? (int)cluster.block_rank() : 0, hk = blockIdx.x / CLUSTER;
   const float* acc = a.acc + hk * a.w_stride;
   const int* ids = a.ids + hk * a.w_stride;
-  // this CTA's slots [s0, s1), and a warp's part [w0, w1) of them
+  // this CTA's slots [s0, s1), and the thread's part [t0, t1) of them
   const int slice = ((a.n + CLUSTER - 1) / CLUSTER + 31) & ~31;
   const int s0 = min(a.n, rank * slice), s1 = min(a.n, s0 + slice);
-  const int part = ((slice + kWarps - 1) / kWarps + 31) & ~31;
-  const int w0 = min(s1, s0 + warp * part), w1 = min(s1, w0 + part);
-  auto key_of = [&](int slot) -> uint32_t {
-    return IN_SMEM ? s_keys[slot - s0] : sort_key(acc[slot], ids[slot], a.recent_from);
-  };
-  if (IN_SMEM)
-    for (int s = s0 + tid; s < s1; s += kThreads) s_keys[s - s0] = sort_key(acc[s], ids[s], a.recent_from);
+  const int part = ((s1 - s0 + kThreads - 1) / kThreads) | 1;
+  const int t0 = min(s1, s0 + tid * part), t1 = min(s1, t0 + part);
+  auto key_of = [&](int slot) -> uint32_t { return sort_key(acc[slot], ids[slot], a.recent_from); };
+  auto top_of = [&](int slot) -> uint32_t { return IN_SMEM ? s_top[slot - s0] : key_of(slot) >> 16; };
+  if (IN_SMEM) {
+#pragma unroll 8
+    for (int s = s0 + tid; s < s1; s += kThreads) s_top[s - s0] = (uint16_t)(key_of(s) >> 16);
+  }
+  for (int b = tid; b < BINS; b += kThreads) {
+    sh.counts[b] = 0;
+    sh.sums[0][b] = 0;
+  }
+  sync_all();
 
   // the n_keep-th largest key: its leading bits are settled pass by pass
   uint32_t prefix = 0, mask = 0, want = (uint32_t)a.keep;
@@ -102,46 +144,45 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const EvictArgs a) 
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = shifts[pass];
     const uint32_t bins = pass == 2 ? 1024u : 2048u;
-    for (int b = tid; b < BINS; b += kThreads) sh.hist[b] = 0;
+    uint32_t run_bin = 0, run = 0;  // equal digits seen in a row
+    auto flush = [&]() {
+      if (run) atomicAdd(&sh.counts[run_bin], run);
+    };
+#pragma unroll 4
+    for (int slot = s0 + tid; slot < s1; slot += kThreads) {
+      uint32_t k = top_of(slot) << 16;
+      if ((k ^ prefix) & mask & 0xffff0000u) continue;
+      if (pass > 0) {
+        k = key_of(slot);
+        if ((k ^ prefix) & mask) continue;
+      }
+      const uint32_t bin = (k >> shift) & (bins - 1);
+      if (bin != run_bin) {
+        flush();
+        run = 0;
+        run_bin = bin;
+      }
+      ++run;
+    }
+    flush();
     __syncthreads();
-    for (int base = w0; base < w1; base += 32) {
-      const int slot = base + lane;
-      bool in = slot < w1;
-      uint32_t bin = 0;
-      if (in) {
-        const uint32_t k = key_of(slot);
-        in = (k & mask) == prefix;
-        bin = (k >> shift) & (bins - 1);
-      }
-      // many equal keys would queue up at one counter
-      const uint32_t live = __ballot_sync(0xffffffffu, in);
-      if (live == 0) continue;
-      const uint32_t first = __shfl_sync(0xffffffffu, bin, __ffs(live) - 1);
-      if (__all_sync(0xffffffffu, !in || bin == first)) {
-        if (lane == 0) atomicAdd(&sh.hist[first], (uint32_t)__popc(live));
-      } else if (in) {
-        atomicAdd(&sh.hist[bin], 1u);
-      }
-    }
-    cluster.sync();
-    // every CTA sums all histograms, two bins a thread from the top, and finds
-    // the bin in which the count from above reaches `want`
-    uint32_t c0 = 0, c1 = 0;
-    const int hi = (int)bins - 1 - 2 * tid;
-    if (hi > 0)
-      for (int r = 0; r < CLUSTER; ++r) {
-        const uint32_t* h = cluster.map_shared_rank(sh.hist, r);
-        c0 += h[hi];
-        c1 += h[hi - 1];
-      }
-    uint32_t sum = c0 + c1, total;
+    // to every CTA's sums; the counts and the other sums are cleared for the next pass
+    uint32_t* sums = sh.sums[pass & 1];
+    for (int b = tid; b < BINS; b += kThreads) {
+      const uint32_t c = sh.counts[b];
+      sh.counts[b] = 0;
+      sh.sums[(pass & 1) ^ 1][b] = 0;
+      if (c) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += y;
+        for (int r = 0; r < CLUSTER; ++r) atomicAdd(of_rank(sums, r) + b, c);
+      }
     }
-    const uint32_t warp_total = __shfl_sync(0xffffffffu, sum, 31);
-    const uint32_t above = warps_before(warp_total, sh.warp_sum, &total) + sum - (c0 + c1);
+    sync_all();
+    // two bins a thread from the top: the one in which the count reaches `want`
+    const int hi = (int)bins - 1 - 2 * tid;
+    const uint32_t c0 = hi > 0 ? sums[hi] : 0, c1 = hi > 0 ? sums[hi - 1] : 0;
+    uint32_t total;
+    const uint32_t above = threads_before(c0 + c1, sh.warp_sum, &total);
     if (above < want && above + c0 >= want) {
       sh.bin = hi;
       sh.above = above;
@@ -149,48 +190,51 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const EvictArgs a) 
       sh.bin = hi - 1;
       sh.above = above + c0;
     }
-    cluster.sync();  // the result is there, and nobody reads a histogram any more
+    __syncthreads();
     want -= sh.above;
     prefix |= sh.bin << shift;
     mask |= (bins - 1) << shift;
   }
   const uint32_t limit = prefix;  // `want` of the keys that equal it stay
 
-  // equal keys before every warp's part: first in the CTA, then in the cluster
+  const uint32_t limit_top = limit >> 16;
+  // above the limit (2), equal to it (1) or below
+  auto rank_of = [&](int slot) -> int {
+    const uint32_t t = top_of(slot);
+    if (t != limit_top) return t > limit_top ? 2 : 0;
+    const uint32_t k = key_of(slot);
+    return k > limit ? 2 : (k == limit ? 1 : 0);
+  };
+  // equal keys before the thread's part: in the CTA, then in the cluster
   uint32_t eq = 0, total;
-  for (int base = w0; base < w1; base += 32)
-    eq += __popc(__ballot_sync(0xffffffffu, base + lane < w1 && key_of(base + lane) == limit));
-  uint32_t eq_before = warps_before(eq, sh.warp_sum, &total);
+  for (int slot = t0; slot < t1; ++slot) eq += rank_of(slot) == 1;
+  uint32_t eq_before = threads_before(eq, sh.warp_sum, &total);
   if (tid == 0) sh.tot[0] = total;
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) eq_before += cluster.map_shared_rank(sh.tot, r)[0];
+  sync_all();
+  for (int r = 0; r < rank; ++r) eq_before += of_rank(sh.tot, r)[0];
 
   // free slots below `keep`, and kept tokens at or behind it
-  const uint32_t below = (1u << lane) - 1;
-  auto kept_ballot = [&](int base, uint32_t* run) -> uint32_t {
-    const int slot = base + lane;
-    const uint32_t k = slot < w1 ? key_of(slot) : 0u;
-    const uint32_t same = __ballot_sync(0xffffffffu, slot < w1 && k == limit);
-    const bool kept = slot < w1 && (k > limit || (k == limit && *run + __popc(same & below) < want));
-    *run += __popc(same);
-    return __ballot_sync(0xffffffffu, kept);
-  };
   uint32_t holes = 0, movers = 0, run = eq_before;
-  for (int base = w0; base < w1; base += 32) {
-    const uint32_t kept = kept_ballot(base, &run);
-    const int slot = base + lane;
-    const uint32_t low = __ballot_sync(0xffffffffu, slot < a.keep && slot < w1);
-    holes += __popc(low & ~kept);
-    movers += __popc(kept & ~low);
+  auto kept = [&](int slot) -> bool {
+    const int x = rank_of(slot);
+    const bool stays = x == 2 || (x == 1 && run < want);
+    run += x == 1;
+    return stays;
+  };
+  for (int slot = t0; slot < t1; ++slot) {
+    const bool stays = kept(slot);
+    holes += slot < a.keep && !stays;
+    movers += slot >= a.keep && stays;
   }
-  uint32_t holes_before = warps_before(holes, sh.warp_sum, &total);
+  uint32_t holes_before = threads_before(holes, sh.warp_sum, &total);
   if (tid == 0) sh.tot[1] = total;
-  uint32_t movers_before = warps_before(movers, sh.warp_sum, &total);
+  uint32_t movers_before = threads_before(movers, sh.warp_sum, &total);
   if (tid == 0) sh.tot[2] = total;
-  cluster.sync();
+  sync_all();
   uint32_t all = 0;
+#pragma unroll
   for (int r = 0; r < CLUSTER; ++r) {
-    const uint32_t* t = cluster.map_shared_rank(sh.tot, r);
+    const uint32_t* t = of_rank(sh.tot, r);
     if (r < rank) {
       holes_before += t[1];
       movers_before += t[2];
@@ -199,26 +243,13 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const EvictArgs a) 
   }
   if (rank == 0 && tid == 0) a.n_moves[hk] = (int)all;
   run = eq_before;
-  for (int base = w0; base < w1; base += 32) {
-    const uint32_t kept = kept_ballot(base, &run);
-    const int slot = base + lane;
-    const bool in = slot < w1, mine = kept >> lane & 1;
-    const uint32_t low = __ballot_sync(0xffffffffu, slot < a.keep && in);
-    const uint32_t free_here = low & ~kept, move_here = kept & ~low;
-    if (in && slot < a.keep) {
-      if (mine) {
-        a.acc_out[hk * a.w_stride + slot] = acc[slot];
-        a.ids_out[hk * a.w_stride + slot] = ids[slot];
-      } else {
-        a.dst[(long long)hk * a.most + holes_before + __popc(free_here & below)] = slot;
-      }
-    } else if (mine) {
-      a.src[(long long)hk * a.most + movers_before + __popc(move_here & below)] = slot;
-    }
-    holes_before += __popc(free_here);
-    movers_before += __popc(move_here);
+  const long long list = (long long)hk * a.most;
+  for (int slot = t0; slot < t1; ++slot) {
+    const bool stays = kept(slot);
+    if (slot < a.keep && !stays) a.dst[list + holes_before++] = slot;
+    if (slot >= a.keep && stays) a.src[list + movers_before++] = slot;
   }
-  cluster.sync();  // no CTA leaves while another may read its shared memory
+  sync_all();  // no CTA leaves while another may read its shared memory
 }
 
 constexpr int MOVE_THREADS = 256, MOVE_UNROLL = 4;
@@ -226,9 +257,11 @@ constexpr int MOVE_BLOCK = MOVE_THREADS / 8 * MOVE_UNROLL;  // moves of a block
 
 __global__ void __launch_bounds__(MOVE_THREADS)
     move_kernel(const EvictArgs a, bf16* __restrict__ k, bf16* __restrict__ v, long long k_stride, long long v_stride) {
-  const int hk = blockIdx.y, e = (threadIdx.x & 7) * 8, grp = threadIdx.x >> 3;
+  // heads vary fastest: equal ranks of all heads lie near one another in memory
+  const int hk = blockIdx.x % a.Hk, e = (threadIdx.x & 7) * 8, grp = threadIdx.x >> 3;
+  const int m0 = blockIdx.x / a.Hk * MOVE_BLOCK;
+  pdl_wait();
   const int n = a.n_moves[hk];
-  const int m0 = blockIdx.x * MOVE_BLOCK;
   if (m0 >= n) return;
   uint4 kk[MOVE_UNROLL], vv[MOVE_UNROLL];
   int to[MOVE_UNROLL];
@@ -253,12 +286,16 @@ __global__ void __launch_bounds__(MOVE_THREADS)
     }
 }
 
-template <bool IN_SMEM>
-cudaError_t launch_select(const EvictArgs& a, size_t smem, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(select_kernel<IN_SMEM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+int slice_of(int n, int cluster) { return ((n + cluster - 1) / cluster + 31) & ~31; }
+
+template <int CLUSTER, bool IN_SMEM>
+cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {
+  const size_t smem = IN_SMEM ? (size_t)slice_of(a.n, CLUSTER) * 2 : 0;
+  cudaError_t e = cudaFuncSetAttribute(select_kernel<CLUSTER, IN_SMEM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kMaxKeys * 2);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.Hk * CLUSTER));
+  cfg.gridDim = dim3((unsigned)(a.Hk * CLUSTER + kCopyCtas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -268,8 +305,8 @@ cudaError_t launch_select(const EvictArgs& a, size_t smem, cudaStream_t st) {
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<IN_SMEM>, a);
+  cfg.numAttrs = CLUSTER > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, select_kernel<CLUSTER, IN_SMEM>, a);
 }
 
 }  // namespace
@@ -291,13 +328,12 @@ cudaError_t launch_cache_evict(const EvictDims& d, bf16* k, bf16* v, const float
   a.n_moves = n_moves;
   a.src = src;
   a.dst = dst;
-  const int slice = ((d.n + CLUSTER - 1) / CLUSTER + 31) & ~31;
-  const cudaError_t e =
-      slice <= kMaxKeys ? launch_select<true>(a, (size_t)slice * 4, st) : launch_select<false>(a, 0, st);
+  const cudaError_t e = d.n <= kFewSlots               ? launch_select<1, true>(a, st)
+                        : slice_of(d.n, 8) <= kMaxKeys ? launch_select<8, true>(a, st)
+                                                       : launch_select<8, false>(a, st);
   if (e != cudaSuccess || a.most == 0) return e;
-  move_kernel<<<dim3((unsigned)((a.most + MOVE_BLOCK - 1) / MOVE_BLOCK), (unsigned)d.Hk), MOVE_THREADS, 0, st>>>(
-      a, k, v, d.k_stride, d.v_stride);
-  return cudaGetLastError();
+  const long long blocks = (long long)((a.most + MOVE_BLOCK - 1) / MOVE_BLOCK) * d.Hk;
+  return launch_second(move_kernel, dim3((unsigned)blocks), MOVE_THREADS, st, a, k, v, d.k_stride, d.v_stride);
 }
 
 }  // namespace gsa

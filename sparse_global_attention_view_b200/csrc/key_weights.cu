@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + OFF_MISC + 4);
   float* sL = reinterpret_cast<float*>(sp + OFF_L);
 
+  pdl_launch();
   const ViewDims& d = a.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int MT = a.rows_tok, tile_rows = MT * d.G;
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256) add_parts_kernel(const WeightsArgs a) {
   const ViewDims& d = a.d;
   const int j = blockIdx.x * 256 + threadIdx.x, hk = blockIdx.y;
+  pdl_wait();
   const long long at = hk * a.acc_out_stride + j;
   if (j < d.n_prefix) {
     if (a.split_prefix < 2) return;
@@ -573,8 +575,8 @@ cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf
     if (e != cudaSuccess) return e;
   }
   if (p.split_prefix > 1 || p.split_own > 1) {
-    add_parts_kernel<<<dim3((unsigned)ceil_div((long long)d.n_prefix + d.n_own, 256), (unsigned)d.Hk), 256, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_second(add_parts_kernel, dim3((unsigned)ceil_div((long long)d.n_prefix + d.n_own, 256), (unsigned)d.Hk),
+                         256, st, a);
   }
   return cudaSuccess;
 }

@@ -24,6 +24,8 @@
 // exponentials, store, two products) is a chain of latencies that only other
 // warps can fill, and with two tiles of 128 x 128 scores and two warps a
 // scheduler the exponential units idled half the time.
+// view_rows_kernel: at most four rows in all against the prefix.  Bound by the read
+// of the cache; CUDA cores, eight lanes a key, four keys' loads in flight a lane.
 // view_own_kernel: views of few rows.  Their own keys are read by CUDA cores
 // (eight lanes a key, plain 16-byte loads: nothing is read that no query sees),
 // and the partial results against the prefix are merged in the same pass.
@@ -100,6 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + OFF_MISC + 4);
 
+  pdl_launch();
   const ViewDims& d = a.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.y;
@@ -526,6 +529,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const ViewDims d, int parts,
   const int e = (threadIdx.x & 7) * 8;
   const long long n = (long long)d.n_q * d.H;
   if (rh >= n) return;
+  pdl_wait();
   const int tok = (int)(rh / d.H), h = (int)(rh - (long long)tok * d.H);
   if (tok < d.q_off[0] || tok >= d.q_off[d.B]) return;
   Merge mg;
@@ -548,10 +552,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const ViewDims d, int parts,
 }
 
 // ---------------------------------------------------------------------------
-// own keys of views with few rows, merged with the prefix's partial results
-
-constexpr int OWN_R = 4;       // rows in registers at a time
-constexpr int OWN_WARPS = 4;
+// CUDA-core kernels: eight lanes hold a key's 64 values
 
 __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -561,6 +562,153 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
     f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
+// Sum over the eight lanes.
+__device__ __forceinline__ float sum8(float s) {
+  s += __shfl_xor_sync(0xffffffffu, s, 1);
+  s += __shfl_xor_sync(0xffffffffu, s, 2);
+  return s + __shfl_xor_sync(0xffffffffu, s, 4);
+}
+
+// A softmax on its way: maximum, sum, and the lane's eight of 64 values.
+struct Row {
+  float m, l, o[8];
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = 0.f;
+  }
+  // joins the states of the lanes that differ in bits 3 and 4
+  __device__ __forceinline__ void join_groups() {
+#pragma unroll
+    for (int x = 8; x <= 16; x <<= 1) {
+      const float mo = __shfl_xor_sync(0xffffffffu, m, x), lo = __shfl_xor_sync(0xffffffffu, l, x);
+      const float mn = fmaxf(m, mo);
+      // equal maxima, two infinite ones among them, need no factor
+      const float ca = m == mn ? 1.f : exp2f(m - mn), cb = mo == mn ? 1.f : exp2f(mo - mn);
+      l = l * ca + lo * cb;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) o[c] = o[c] * ca + __shfl_xor_sync(0xffffffffu, o[c], x) * cb;
+      m = mn;
+    }
+  }
+};
+
+constexpr int ROWS_THREADS = 512, ROWS_UNROLL = 4;
+
+// Block (split, key head): rows [0, R) against the split's part of the prefix.
+template <int R>
+__global__ void __launch_bounds__(ROWS_THREADS)
+    view_rows_kernel(const ViewDims d, const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
+                     float* __restrict__ part_o, float* __restrict__ part_lse) {
+  pdl_launch();
+  constexpr int WARPS = ROWS_THREADS / 32, GROUPS = ROWS_THREADS / 8;
+  __shared__ float s_m[WARPS][R], s_l[WARPS][R], s_o[WARPS][R][64];
+  const int hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = (lane & 7) * 8;
+  const int rows = d.n_q * d.G;
+  const int j0 = (int)((long long)d.n_prefix * blockIdx.x / gridDim.x);
+  const int j1 = (int)((long long)d.n_prefix * (blockIdx.x + 1) / gridDim.x);
+  float qf[R][8];
+  Row st[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int row = min(i, rows - 1), tl = row / d.G, h = hk * d.G + row - tl * d.G;
+    unpack8(*reinterpret_cast<const uint4*>(q + tl * d.q_stride + h * 64 + e), qf[i]);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) qf[i][c] *= d.c2;
+    st[i].clear();
+  }
+  const bf16* kb = k + hk * 64 + e;
+  const bf16* vb = v + hk * 64 + e;
+  for (int base = j0 + (tid >> 3); base < j1 + (tid >> 3); base += GROUPS * ROWS_UNROLL) {
+    uint4 ku[ROWS_UNROLL], vu[ROWS_UNROLL];
+#pragma unroll
+    for (int u = 0; u < ROWS_UNROLL; ++u) {
+      const int j = base + u * GROUPS;
+      ku[u] = vu[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (j < j1) {
+        ku[u] = *reinterpret_cast<const uint4*>(kb + j * d.kp_stride);
+        vu[u] = *reinterpret_cast<const uint4*>(vb + j * d.vp_stride);
+      }
+    }
+    float s[R][ROWS_UNROLL];
+#pragma unroll
+    for (int u = 0; u < ROWS_UNROLL; ++u) {
+      float kf[8];
+      unpack8(ku[u], kf);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float x = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x = fmaf(qf[i][c], kf[c], x);
+        x = sum8(x);
+        s[i][u] = base + u * GROUPS < j1 ? x : -INFINITY;
+      }
+    }
+    float p[R][ROWS_UNROLL];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float mn = st[i].m;
+#pragma unroll
+      for (int u = 0; u < ROWS_UNROLL; ++u) mn = fmaxf(mn, s[i][u]);
+      const float corr = st[i].m == mn ? 1.f : exp2f(st[i].m - mn);
+      st[i].m = mn;
+      st[i].l *= corr;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) st[i].o[c] *= corr;
+#pragma unroll
+      for (int u = 0; u < ROWS_UNROLL; ++u) {
+        p[i][u] = s[i][u] == -INFINITY ? 0.f : exp2f(s[i][u] - mn);
+        st[i].l += p[i][u];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < ROWS_UNROLL; ++u) {
+      float vf[8];
+      unpack8(vu[u], vf);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) st[i].o[c] = fmaf(p[i][u], vf[c], st[i].o[c]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    st[i].join_groups();
+    if (lane < 8) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s_o[warp][i][e + c] = st[i].o[c];
+      if (lane == 0) {
+        s_m[warp][i] = st[i].m;
+        s_l[warp][i] = st[i].l;
+      }
+    }
+  }
+  __syncthreads();
+  // thread (row, value): joins the warps
+  const int i = tid >> 6, c = tid & 63;
+  if (i < min(R, rows)) {
+    float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w][i]);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = s_m[w][i] == m ? 1.f : exp2f(s_m[w][i] - m);
+      l += s_l[w][i] * f;
+      o += s_o[w][i][c] * f;
+    }
+    const int tl = i / d.G, h = hk * d.G + i - tl * d.G;
+    const long long at = ((long long)blockIdx.x * d.n_q + tl) * d.H + h;
+    part_o[at * 64 + c] = l == 0.f ? 0.f : o / l;
+    if (c == 0) part_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// own keys of views with few rows, merged with the prefix's partial results
+
+constexpr int OWN_R = 4;       // rows in registers at a time
+constexpr int OWN_WARPS = 4;
 
 // One block = one view and key head.  Eight lanes hold a key's 64 values; the
 // block's 16 groups of eight take the keys in turn, each with a softmax of its
@@ -577,21 +725,17 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
   const int nq = r.q1 - r.q0, nk = r.k1 - r.k0, rows = nq * d.G;
   const long long n = (long long)d.n_q * d.H;
   for (int r0 = 0; r0 < rows; r0 += OWN_R) {
-    float qf[OWN_R][8], o[OWN_R][8], m[OWN_R], l[OWN_R];
+    float qf[OWN_R][8];
+    Row st[OWN_R];
     int end[OWN_R];
     int end_max = 0;
 #pragma unroll
     for (int i = 0; i < OWN_R; ++i) {
       const int row = min(r0 + i, rows - 1), tl = row / d.G, h = hk * d.G + row - tl * d.G;
-      const uint4 u = *reinterpret_cast<const uint4*>(q + (r.q0 + tl) * d.q_stride + h * 64 + e);
-      unpack8(u, qf[i]);
+      unpack8(*reinterpret_cast<const uint4*>(q + (r.q0 + tl) * d.q_stride + h * 64 + e), qf[i]);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        qf[i][c] *= d.c2;
-        o[i][c] = 0.f;
-      }
-      m[i] = -CUDART_INF_F;
-      l[i] = 0.f;
+      for (int c = 0; c < 8; ++c) qf[i][c] *= d.c2;
+      st[i].clear();
       end[i] = d.causal ? max(0, min(nk, tl + nk - nq + 1)) : nk;
       end_max = max(end_max, end[i]);
     }
@@ -609,78 +753,68 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
         float s = 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) s = fmaf(qf[i][c], kf[c], s);
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        s += __shfl_xor_sync(0xffffffffu, s, 4);
+        s = sum8(s);
         if (j < end[i]) {
           // exp2f(-infinity - -infinity) would be NaN for scores of -infinity
-          const float mn = fmaxf(m[i], s);
-          const float corr = m[i] == mn ? 1.f : exp2f(m[i] - mn);
+          const float mn = fmaxf(st[i].m, s);
+          const float corr = st[i].m == mn ? 1.f : exp2f(st[i].m - mn);
           const float p = s == -CUDART_INF_F ? 0.f : exp2f(s - mn);
-          l[i] = l[i] * corr + p;
+          st[i].l = st[i].l * corr + p;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) o[i][c] = fmaf(p, vf[c], o[i][c] * corr);
-          m[i] = mn;
+          for (int c = 0; c < 8; ++c) st[i].o[c] = fmaf(p, vf[c], st[i].o[c] * corr);
+          st[i].m = mn;
         }
       }
     }
     // the four groups of the warp, then the warps
 #pragma unroll
     for (int i = 0; i < OWN_R; ++i) {
-#pragma unroll
-      for (int x = 8; x <= 16; x <<= 1) {
-        const float mo = __shfl_xor_sync(0xffffffffu, m[i], x), lo = __shfl_xor_sync(0xffffffffu, l[i], x);
-        const float mn = fmaxf(m[i], mo);
-        const float ca = m[i] == mn ? 1.f : exp2f(m[i] - mn), cb = mo == mn ? 1.f : exp2f(mo - mn);
-        l[i] = l[i] * ca + lo * cb;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float oo = __shfl_xor_sync(0xffffffffu, o[i][c], x);
-          o[i][c] = o[i][c] * ca + oo * cb;
-        }
-        m[i] = mn;
-      }
+      st[i].join_groups();
       if (lane < 8) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) s_o[warp][i][e + c] = o[i][c];
+        for (int c = 0; c < 8; ++c) s_o[warp][i][e + c] = st[i].o[c];
         if (lane == 0) {
-          s_m[warp][i] = m[i];
-          s_l[warp][i] = l[i];
+          s_m[warp][i] = st[i].m;
+          s_l[warp][i] = st[i].l;
         }
       }
     }
     __syncthreads();
-    // warp i: row i; lanes 0-7 carry it on with the prefix's results
-    if (lane < 8 && warp < OWN_R && r0 + warp < rows) {
-      const int row = r0 + warp, tl = row / d.G, h = hk * d.G + row - tl * d.G, tok = r.q0 + tl;
-      Merge mg;
-      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (parts > 0 && r0 == 0) pdl_wait();
+    // warp i: row i.  Its four groups take the own results of a warp each, and the
+    // prefix's in turn
+    const bool mine = r0 + warp < rows;
+    Row x;
+    x.clear();
+    const int row = min(r0 + warp, rows - 1), tl = row / d.G, h = hk * d.G + row - tl * d.G, tok = r.q0 + tl;
+    const long long rh = (long long)tok * d.H + h;
+    x.m = s_m[lane >> 3][warp];
+    x.l = s_l[lane >> 3][warp];
 #pragma unroll
-      for (int w = 0; w < OWN_WARPS; ++w) {
-        const float lw = s_l[w][warp], mw = s_m[w][warp];
-        if (lw == 0.f) continue;
-        float keep, wt;
-        if (!mg.add(mw + log2f(lw), &keep, &wt)) continue;
-        const float f = wt / lw;
+    for (int c = 0; c < 8; ++c) x.o[c] = s_o[lane >> 3][warp][e + c];
+#pragma unroll 2
+    for (int p = lane >> 3; p < parts; p += 4) {
+      const float z = part_lse[p * n + rh];
+      const float4* src = reinterpret_cast<const float4*>(part_o + (p * n + rh) * 64 + e);
+      const float4 y0 = src[0], y1 = src[1];
+      if (z == -INFINITY) continue;  // nothing was written
+      const float pv[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+      const float mn = fmaxf(x.m, z);
+      const float ca = x.m == mn ? 1.f : exp2f(x.m - mn), cb = z == mn ? 1.f : exp2f(z - mn);
+      x.l = x.l * ca + cb;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = acc[c] * keep + s_o[w][warp][e + c] * f;
-      }
-      const long long rh = (long long)tok * d.H + h;
-      for (int p = 0; p < parts; ++p) {
-        float keep, wt;
-        if (!mg.add(part_lse[p * n + rh], &keep, &wt)) continue;
-        const float4* src = reinterpret_cast<const float4*>(part_o + (p * n + rh) * 64 + e);
-        const float4 x = src[0], y = src[1];
-        const float pv[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = acc[c] * keep + pv[c] * wt;
-      }
-      const float inv = mg.inv();
+      for (int c = 0; c < 8; ++c) x.o[c] = x.o[c] * ca + pv[c] * cb;
+      x.m = mn;
+    }
+    x.join_groups();
+    if (mine && lane < 8) {
+      const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
       uint32_t w[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) w[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+      for (int c = 0; c < 4; ++c)
+        w[c] = x.l == 0.f ? 0u : pack_bf16x2(x.o[2 * c] * inv, x.o[2 * c + 1] * inv);
       *reinterpret_cast<uint4*>(out + tok * d.o_stride + h * 64 + e) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (lse && e == 0) lse[rh] = mg.lse();
+      if (lse && e == 0) lse[rh] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * 0.6931471805599453f;
     }
     __syncthreads();
   }
@@ -731,6 +865,15 @@ ViewPlan view_plan(const ViewDims& d) {
   }
   // partial results of one launch of a kind: their bytes against a key tile's time
   const double merge = 1.0 + (double)d.n_q * d.H * 64 * 8 / 3.0e6;
+  p.rows = p.packed && (long long)d.n_q * d.G <= 4 && (p.small_own || !has_own);
+  if (p.rows) {
+    // a block an SM, of 128 keys at least
+    int s = 148 / d.Hk;
+    if (s > d.n_prefix / 128) s = d.n_prefix / 128;
+    p.split_packed = s > 1 ? s : 1;
+    p.parts = p.split_packed;
+    return p;
+  }
   if (p.packed) {
     const long long units = (long long)ceil_div(d.n_q, 2 * MT) * d.Hk;
     p.split_packed = choose_split(units, np, 64, 4.0, merge);
@@ -754,7 +897,18 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
                                unsigned* err, cudaStream_t st) {
   if (d.n_q <= 0) return cudaSuccess;
   const int MT = 128 / d.G;
-  if (p.packed || p.aligned) {
+  if (p.rows) {
+    const dim3 grid((unsigned)p.split_packed, (unsigned)d.Hk);
+    const int rows = d.n_q * d.G;
+    if (rows == 1)
+      view_rows_kernel<1><<<grid, ROWS_THREADS, 0, st>>>(d, q, kp, vp, part_o, part_lse);
+    else if (rows == 2)
+      view_rows_kernel<2><<<grid, ROWS_THREADS, 0, st>>>(d, q, kp, vp, part_o, part_lse);
+    else
+      view_rows_kernel<4><<<grid, ROWS_THREADS, 0, st>>>(d, q, kp, vp, part_o, part_lse);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  } else if (p.packed || p.aligned) {
     cudaError_t e = prepare_kernel();
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mkp, mvp, mko, mvo;
@@ -806,14 +960,17 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
     }
   }
   if (p.small_own) {
-    view_own_kernel<<<dim3((unsigned)d.B, (unsigned)d.Hk), 32 * OWN_WARPS, 0, st>>>(d, q, ko, vo, p.parts, part_o, part_lse,
-                                                                                  out, lse, err);
+    const dim3 grid((unsigned)d.B, (unsigned)d.Hk);
+    if (p.parts > 0)
+      return launch_second(view_own_kernel, grid, 32 * OWN_WARPS, st, d, q, ko, vo, p.parts, (const float*)part_o,
+                           (const float*)part_lse, out, lse, err);
+    view_own_kernel<<<grid, 32 * OWN_WARPS, 0, st>>>(d, q, ko, vo, 0, part_o, part_lse, out, lse, err);
     return cudaGetLastError();
   }
   if (p.parts > 0 || (!p.packed && !p.aligned)) {
     const long long blocks = ((long long)d.n_q * d.H * 8 + 255) / 256;
-    merge_kernel<<<(unsigned)blocks, 256, 0, st>>>(d, p.parts, part_o, part_lse, out, lse);
-    return cudaGetLastError();
+    return launch_second(merge_kernel, dim3((unsigned)blocks), 256, st, d, p.parts, (const float*)part_o,
+                         (const float*)part_lse, out, lse);
   }
   return cudaSuccess;
 }

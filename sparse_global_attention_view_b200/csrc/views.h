@@ -25,6 +25,7 @@ struct ViewPlan {
   // the tensor-core launches: rows packed over views against the prefix
   // alone, rows aligned to views against both, or against their own keys alone
   int packed, aligned, aligned_prefix, aligned_own;
+  int rows;        // at most four rows: the prefix by the CUDA-core kernel, instead of `packed`
   int small_own;   // the views' own keys by the CUDA-core kernel, which also merges
   int split_packed, split_aligned;  // key splits
   int parts;       // partial results per (query, head); 0: written directly
@@ -55,6 +56,26 @@ struct EvictDims {
 inline int evict_most_moves(const EvictDims& d) { return d.keep < d.n - d.keep ? d.keep : d.n - d.keep; }
 cudaError_t launch_cache_evict(const EvictDims& d, bf16* k, bf16* v, const float* acc, const int* ids, float* acc_out,
                                int* ids_out, int* n_moves, int* src, int* dst, cudaStream_t st);
+
+// A second kernel of a call: launched while the first one still runs, so that its
+// start is not waited for.  The first kernel calls pdl_launch() at its start, the
+// second one pdl_wait() before it touches memory: it goes on when the first one has
+// ended and its writes are visible.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_second(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 
 // A view's ranges; false (and the device-check bit) when the offsets do not
 // describe rows of the buffers or more of them than a view may have.

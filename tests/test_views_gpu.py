@@ -71,6 +71,9 @@ SIZES = {
     "one token": (2, 2, [1], [1], 5),
     "one token, no prefix": (2, 2, [1], [1], 0),
     "one token, no own": (4, 2, [1], [0], 1374),
+    "three rows": (3, 1, [1], [7], 1300),
+    "four tokens": (2, 2, [1, 2, 1], [7, 0, 130], 1300),
+    "five tokens": (2, 2, [1, 3, 1], [7, 0, 130], 300),
     "no keys": (2, 2, [3, 130], [0, 0], 0),
     "views without keys": (2, 2, [3, 2, 0, 1], [0, 5, 4, 0], 0),
     "long token": (16, 16, [1], [1], 13740),
@@ -178,7 +181,8 @@ def evict(k, v, acc, ids, keep, recent_from, n=None):
 
 @pytest.mark.parametrize("ties", [False, True])
 @pytest.mark.parametrize("heads,n,keep", [(1, 1, 1), (2, 2, 1), (1, 31, 7), (3, 33, 32), (2, 257, 256), (16, 1705, 1374),
-                                          (2, 5000, 1), (2, 5000, 4999), (2, 5000, 5000), (4, 8191, 4096), (1, 40000, 20001)])
+                                          (2, 5000, 1), (2, 5000, 4999), (2, 5000, 5000), (4, 8191, 4096), (1, 40000, 20001), (2, 8193, 3000),
+                                          (3, 8192, 7)])
 def test_evict(heads, n, keep, ties):
     k, v, acc, ids = cache(heads, n, n + keep, ties)
     for recent in (0, min(keep, 5), keep, n):
@@ -198,8 +202,8 @@ def test_evict_of_special_values():
 
 def test_evict_beyond_shared_memory():
     # a slice of a head's slots that does not fit a CTA's shared memory
-    k, v, acc, ids = cache(1, 8 * 40 * 1024 + 1000, 5, True)
-    assert_evicted(k, v, acc, ids, 200_000, 400_000, *evict(k, v, acc, ids, 200_000, 400_000))
+    k, v, acc, ids = cache(1, 8 * 96 * 1024 + 1000, 5, True)
+    assert_evicted(k, v, acc, ids, 200_000, 800_000, *evict(k, v, acc, ids, 200_000, 800_000))
 
 
 def test_evict_twice_is_evict_once():
