@@ -19,6 +19,7 @@
 // exponential as in attention, and no maximum, packing or store of weights).
 // Few items are cut over query ranges, whose sums are added in order afterwards.
 //
+// key_weights_own_kernel: the own keys of views of few rows, eight lanes a key.
 // key_weights_rows_kernel: at most eight rows in all.  Bound by the read of the
 // keys; eight lanes hold a key, and after the dot products lane r takes the
 // exponential of row r.
@@ -59,8 +60,10 @@ struct WeightsArgs {
   ViewDims d;
   int rows_tok;                       // tokens per query tile: 128 / G
   int prefix_units, own_units;        // items of 512 keys: of the prefix, of one view at most
+  int prefix_items;                   // items that come before the views' own
   int split_prefix, split_own;        // query ranges of an item
   int n_items;
+  uint32_t m_units, m_split, m_tok;   // for quotients by prefix_units, split_prefix and rows_tok (udiv31)
   const float* lse;                   // [n_q][H]
   const float* acc;                   // nullable [Hk][acc_stride]
   float* acc_out;                     // [Hk][acc_out_stride]
@@ -84,30 +87,32 @@ struct Item {
 __device__ __forceinline__ Item get_item(const WeightsArgs& a, int idx, bool report) {
   const ViewDims& d = a.d;
   Item it;
-  const int per_head = a.prefix_units * a.split_prefix + d.B * a.own_units * a.split_own;
-  it.hk = idx / per_head;
-  int r = idx - it.hk * per_head;
   it.n_keys = 0;
   it.tiles = 0;
   it.see0 = -2147483647;
   int n_split;
-  it.own = r >= a.prefix_units * a.split_prefix;
+  // the prefix's items first: they are the longer ones
+  it.own = idx >= a.prefix_items;
   if (!it.own) {
     n_split = a.split_prefix;
-    it.split = r / a.prefix_units;
-    it.key0 = (r - it.split * a.prefix_units) * ITEM;
+    const int r = udiv31(idx, a.prefix_units, a.m_units);
+    it.hk = udiv31(r, a.split_prefix, a.m_split);
+    it.split = r - it.hk * a.split_prefix;
+    it.key0 = (idx - r * a.prefix_units) * ITEM;
     it.n_keys = min(ITEM, d.n_prefix - it.key0);
     it.tok_lo = max(d.q_off[0], 0);
     it.tok_hi = min(d.q_off[d.B], d.n_q);
     it.tok0 = 0;
   } else {
-    r -= a.prefix_units * a.split_prefix;
     n_split = a.split_own;
-    it.split = r / (d.B * a.own_units);
-    r -= it.split * d.B * a.own_units;
-    const int b = r / a.own_units, u = r - b * a.own_units;
+    int r = (idx - a.prefix_items) / a.own_units;
+    const int u = idx - a.prefix_items - r * a.own_units;
+    it.hk = r / (a.split_own * d.B);
+    r -= it.hk * a.split_own * d.B;
+    it.split = r / d.B;
+    const int b = r - it.split * d.B;
     ViewRange v;
-    if (report ? !view_range(d, b, &v, a.err) : !view_range(d, b, &v, nullptr)) return it;
+    if (!view_range(d, b, &v, report ? a.err : nullptr)) return it;
     const int nk = v.k1 - v.k0, nq = v.q1 - v.q0;
     if (u * ITEM >= nk) return it;
     it.key0 = v.k0 + u * ITEM;
@@ -120,9 +125,10 @@ __device__ __forceinline__ Item get_item(const WeightsArgs& a, int idx, bool rep
       it.tok0 += max(0, it.see0 - v.q0) / a.rows_tok * a.rows_tok;
     }
   }
-  const int all = max(0, (it.tok_hi - it.tok0 + a.rows_tok - 1) / a.rows_tok);
-  const int t0 = (int)((long long)all * it.split / n_split);
-  it.tiles = (int)((long long)all * (it.split + 1) / n_split) - t0;
+  // at most 2^24 tiles and 32 ranges
+  const int all = udiv31(max(0, it.tok_hi - it.tok0 + a.rows_tok - 1), a.rows_tok, a.m_tok);
+  const int t0 = n_split == 1 ? 0 : all * it.split / n_split;
+  it.tiles = n_split == 1 ? all : all * (it.split + 1) / n_split - t0;
   it.tok0 += t0 * a.rows_tok;
   return it;
 }
@@ -207,44 +213,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = max(0, step - ST); k < step; ++k) mbar_wait(bar(B_QF + k % ST), (k / ST) & 1, &never, a.err);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id = idesc(128, 128, kFmtBF16, 0, 0);
-      int it_n = 0, step = 0;
-      uint32_t se_seen = 0;  // a bit for each slot: parity of its next free-wait
-      uint32_t se_used = 0;  // slots that have been written before
-      bool ok = true;
-      for (int idx = blockIdx.x; ok && idx < a.n_items; idx += gridDim.x) {
-        const Item it = get_item(a, idx, false);
-        if (it.n_keys == 0 || it.tiles == 0) continue;
-        const int kb = it_n & 1, slots = (it.n_keys + 127) / 128;
-        if (!(ok = wait(B_KF + kb, (it_n >> 1) & 1))) break;
-        for (int i = 0; ok && i < it.tiles; ++i, ++step) {
-          const int s = step % ST;
-          if (!(ok = wait(B_QF + s, (step / ST) & 1))) break;
-          for (int t = 0; t < slots; ++t) {
-            if (se_used >> t & 1) {
-              if (!(ok = wait(B_SE + t, se_seen >> t & 1))) break;
-              se_seen ^= 1u << t;
-            }
-            se_used |= 1u << t;
-            fence_after_sync();
+    // the whole warp runs the loop and one lane issues
+    const bool leader = elect_one();
+    const uint32_t id = idesc(128, 128, kFmtBF16, 0, 0);
+    const uint64_t k_desc = sdesc_k(sK), q_desc = sdesc_k(sQ);  // count 16-byte units
+    auto all_wait = [&](int b, uint32_t parity) { return warp_wait_fast(bar(b), parity, abort_flag, a.err, limit); };
+    int it_n = 0, step = 0;
+    uint32_t se_seen = 0;  // a bit for each slot: parity of its next free-wait
+    uint32_t se_used = 0;  // slots that have been written before
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < a.n_items; idx += gridDim.x) {
+      const Item it = get_item(a, idx, false);
+      if (it.n_keys == 0 || it.tiles == 0) continue;
+      const int kb = it_n & 1, slots = (it.n_keys + 127) / 128;
+      if (!(ok = all_wait(B_KF + kb, (it_n >> 1) & 1))) break;
+      for (int i = 0; ok && i < it.tiles; ++i, ++step) {
+        const int s = step % ST;
+        if (!(ok = all_wait(B_QF + s, (step / ST) & 1))) break;
+        const uint64_t qd = q_desc + (uint64_t)(s * (kTile >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ss(tbase + t * 128, sdesc_k(sK + (kb * SLOTS + t) * kTile + kk * 32),
-                          sdesc_k(sQ + s * kTile + kk * 32), id, kk > 0);
+        for (int t = 0; t < SLOTS; ++t) {
+          if (t >= slots) break;
+          if (se_used >> t & 1) {
+            if (!(ok = all_wait(B_SE + t, se_seen >> t & 1))) break;
+            se_seen ^= 1u << t;
+          }
+          se_used |= 1u << t;
+          fence_after_sync();
+          const uint64_t kd = k_desc + (uint64_t)((kb * SLOTS + t) * (kTile >> 4));
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_bf16_ss(tbase + t * 128, kd + kk * 2, qd + kk * 2, id, kk > 0);
             mma_commit(bar(B_SF + t));
           }
-          if (ok) mma_commit(bar(B_QE + s));
         }
-        if (ok) mma_commit(bar(B_KE + kb));
-        ++it_n;
+        if (ok && leader) mma_commit(bar(B_QE + s));
       }
-      if (!ok) {
-        // wait for the products already issued before TMEM is released
-        volatile int never = 0;
-        mma_commit(bar(B_DRAIN));
-        mbar_wait(bar(B_DRAIN), 0, &never, a.err);
-      }
+      if (ok && leader) mma_commit(bar(B_KE + kb));
+      ++it_n;
+    }
+    if (!ok) {
+      // wait for the products already issued before TMEM is released
+      volatile int never = 0;
+      if (leader) mma_commit(bar(B_DRAIN));
+      __syncwarp();
+      mbar_wait(bar(B_DRAIN), 0, &never, a.err);
     }
   } else if (warp == 2) {
     int step = 0;
@@ -286,13 +299,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.n_keys == 0) continue;
       const int r = t * 128 + row;  // the thread's key of the item
       const bool slot_live = t * 128 < it.n_keys;
-      float total = 0.f;
+      float total = 0.f, before = 0.f;  // the account so far, on its way during the products
+      if (!it.own && a.acc && a.split_prefix == 1 && r < it.n_keys) before = a.acc[it.hk * a.acc_stride + it.key0 + r];
       for (int i = 0; ok && i < it.tiles; ++i, ++step) {
         const int s = step % ST;
-        ok = __all_sync(0xffffffffu, wait(B_LF + s, (step / ST) & 1));
+        ok = warp_wait_fast(bar(B_LF + s), (step / ST) & 1, abort_flag, a.err, limit);
         if (!ok) break;
         if (slot_live) {
-          ok = __all_sync(0xffffffffu, wait(B_SF + t, sf));
+          ok = warp_wait_fast(bar(B_SF + t), sf, abort_flag, a.err, limit);
           if (!ok) break;
           sf ^= 1;
           fence_after_sync();
@@ -300,18 +314,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tok0 = it.tok0 + i * MT;
           const int lo = max(max(it.tok_lo, it.see0 + r) - tok0, 0) * d.G;
           const int hi = it.tok_hi - tok0 >= MT ? 128 : (it.tok_hi - tok0) * d.G;
-          const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == 128);
+          // rows behind the last query that there is are zeros, and weigh nothing by
+          // their log sum; others may hold anything
+          const bool whole = __all_sync(0xffffffffu, lo == 0 && (hi == 128 || it.tok_hi == d.n_q));
           const float4* nl = reinterpret_cast<const float4*>(sL + s * 128);
           uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
+          uint32_t sv[32];
+          auto chunk = [&](int c) {
+            if (!whole) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t sv[32];
-            tmem_ld32(s_addr + 32 * c, sv);
-            tmem_wait_ld();
-            if (c == 3) {
-              fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(B_SE + t));
+              for (int u = 0; u < 32; ++u)
+                if (32 * c + u < lo || 32 * c + u >= hi) sv[u] = __float_as_uint(-CUDART_INF_F);
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -329,15 +342,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                   f2_unpack(x2, x0, x1);
                   p2 = f2_pack(exp2_mufu(x0), exp2_mufu(x1));
                 }
-                if (!whole) {
-                  float p0, p1;
-                  f2_unpack(p2, p0, p1);
-                  const int col = 32 * c + k;
-                  p2 = f2_pack(col >= lo && col < hi ? p0 : 0.f, col + 1 >= lo && col + 1 < hi ? p1 : 0.f);
-                }
                 ps[(2 * u + w) & 3] = f2_add(ps[(2 * u + w) & 3], p2);
               }
             }
+          };
+          // as far as there are queries (a rolled loop: registers to overlap the
+          // exponentials in, and little code; 943 us at 5496 queries and 46716 keys of
+          // 16 heads against 1159 with the next load in flight)
+          const int chunks = max(1, (min(hi, 128) + 31) >> 5);
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            tmem_ld32(s_addr + 32 * c, sv);
+            tmem_wait_ld();
+            if (c == chunks - 1) {
+              fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(B_SE + t));
+            }
+            chunk(c);
           }
           const uint64_t p01 = f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3]));
           float p0, p1;
@@ -356,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             a.part_prefix[((long long)it.split * d.Hk + it.hk) * d.n_prefix + key] = total;
         } else {
-          if (!it.own && a.acc) total += a.decay * a.acc[it.hk * a.acc_stride + key];
+          if (!it.own && a.acc) total += a.decay * before;
           a.acc_out[it.hk * a.acc_out_stride + (it.own ? d.n_prefix + key : key)] = total;
         }
       }
@@ -486,6 +508,56 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// Own keys of views of few rows: a group of eight lanes takes a key and goes over
+// the queries of its view.
+__global__ void __launch_bounds__(256)
+    key_weights_own_kernel(const WeightsArgs a, const bf16* __restrict__ q, const bf16* __restrict__ k) {
+  const ViewDims& d = a.d;
+  const int hk = blockIdx.y, e = (threadIdx.x & 7) * 8;
+  const int j = blockIdx.x * 32 + (threadIdx.x >> 3);
+  if (blockIdx.x == 0 && hk == 0) {
+    ViewRange r;
+    for (int b = threadIdx.x; b < d.B; b += 256) view_range(d, b, &r, a.err);
+  }
+  const bool in = j < d.n_own && j >= d.own_off[0] && j < d.own_off[d.B];
+  // the view of the key: the last one that starts at or before it
+  int lo = 0, hi = d.B;
+  while (in && hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (d.own_off[mid] <= j) lo = mid; else hi = mid;
+  }
+  int tok = 0, tok_hi = 0;
+  uint4 ku = make_uint4(0u, 0u, 0u, 0u);
+  if (in) {
+    tok = max(d.q_off[lo], 0);
+    tok_hi = min(d.q_off[lo + 1], d.n_q);
+    if (d.causal) tok = max(tok, j - d.own_off[lo + 1] + d.q_off[lo + 1]);
+    ku = *reinterpret_cast<const uint4*>(k + j * d.ko_stride + hk * 64 + e);
+  }
+  float total = 0.f;
+  // the four keys of a warp may have views of different length: all go on to the longest
+  for (int row = tok * d.G; __any_sync(0xffffffffu, row < tok_hi * d.G); ++row) {
+    const bool live = row < tok_hi * d.G;
+    const int t = live ? row / d.G : 0, h = hk * d.G + (live ? row - t * d.G : 0);
+    float qf[8];
+    const uint4 w = *reinterpret_cast<const uint4*>(q + t * d.q_stride + h * 64 + e);
+    const float z = a.lse[(long long)t * d.H + h];
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      qf[2 * c] = __uint_as_float(x[c] << 16);
+      qf[2 * c + 1] = __uint_as_float(x[c] & 0xffff0000u);
+    }
+    float s = dot8(ku, qf);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 4);
+    if (live && z != -CUDART_INF_F) total += exp2_mufu(fmaf(s, d.c2, -z * 1.4426950408889634f));
+  }
+  if (in && e == 0) a.acc_out[hk * a.acc_out_stride + d.n_prefix + j] = total;
+  pdl_wait();  // whoever waits for this kernel waits for the one before it too
+}
+
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 }  // namespace
@@ -499,7 +571,8 @@ WeightsPlan weights_plan(const ViewDims& d) {
   }
   const int MT = 128 / d.G;
   p.prefix_units = ceil_div(d.n_prefix, ITEM);
-  p.own_units = ceil_div(d.max_own, ITEM);
+  p.own_cores = (long long)d.max_q * d.G <= 16;
+  p.own_units = p.own_cores ? 0 : ceil_div(d.max_own, ITEM);
   // query ranges so that the items fill the SMs evenly: an item costs its query
   // tiles and about two more, and there are as many own items as tokens at most
   const int tiles_p = ceil_div(d.n_q, MT), tiles_o = ceil_div(d.max_q, MT);
@@ -547,6 +620,10 @@ cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf
   a.own_units = p.own_units;
   a.split_prefix = p.split_prefix;
   a.split_own = p.split_own;
+  a.prefix_items = p.prefix_units * p.split_prefix * d.Hk;
+  a.m_units = 0xffffffffu / (uint32_t)(p.prefix_units > 0 ? p.prefix_units : 1);
+  a.m_split = 0xffffffffu / (uint32_t)p.split_prefix;
+  a.m_tok = 0xffffffffu / (uint32_t)MT;
   const long long items = ((long long)p.prefix_units * p.split_prefix + (long long)d.B * p.own_units * p.split_own) * d.Hk;
   if (items > 0x7fffffffLL - 1024) return cudaErrorInvalidValue;
   a.n_items = (int)items;
@@ -572,6 +649,14 @@ cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf
     const int grid = a.n_items < 148 ? a.n_items : 148;
     key_weights_kernel<<<(unsigned)grid, kThreads, kSmemBytes, st>>>(mq, mkp, mko, a);
     e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.own_cores && d.n_own > 0) {
+    const dim3 grid((unsigned)ceil_div(d.n_own, 32), (unsigned)d.Hk);
+    if (a.n_items > 0 && p.split_prefix == 1)
+      return launch_second(key_weights_own_kernel, grid, 256, st, a, q, ko);
+    key_weights_own_kernel<<<grid, 256, 0, st>>>(a, q, ko);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (p.split_prefix > 1 || p.split_own > 1) {

@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(ROWS_THREADS)
 constexpr int OWN_R = 4;       // rows in registers at a time
 constexpr int OWN_WARPS = 4;
 
-// One block = one view and key head.  Eight lanes hold a key's 64 values; the
+// One block = one view, key head and four of the view's rows.  Eight lanes hold a key's 64 values; the
 // block's 16 groups of eight take the keys in turn, each with a softmax of its
 // own, merged at the end.
 __global__ void __launch_bounds__(32 * OWN_WARPS)
@@ -719,12 +719,20 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
                     const float* __restrict__ part_lse, bf16* __restrict__ out, float* __restrict__ lse, unsigned* err) {
   const int b = blockIdx.x, hk = blockIdx.y;
   ViewRange r;
-  if (!view_range(d, b, &r, err)) return;
+  if (!view_range(d, b, &r, err)) {
+    pdl_wait();  // whoever waits for this kernel waits for the one before it too
+    return;
+  }
   __shared__ float s_m[OWN_WARPS][OWN_R], s_l[OWN_WARPS][OWN_R], s_o[OWN_WARPS][OWN_R][64];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = (lane & 7) * 8, grp = tid >> 3;
   const int nq = r.q1 - r.q0, nk = r.k1 - r.k0, rows = nq * d.G;
   const long long n = (long long)d.n_q * d.H;
-  for (int r0 = 0; r0 < rows; r0 += OWN_R) {
+  const int r0 = blockIdx.z * OWN_R;
+  if (r0 >= rows) {
+    pdl_wait();
+    return;
+  }
+  {
     float qf[OWN_R][8];
     Row st[OWN_R];
     int end[OWN_R];
@@ -780,7 +788,7 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
       }
     }
     __syncthreads();
-    if (parts > 0 && r0 == 0) pdl_wait();
+    if (parts > 0) pdl_wait();
     // warp i: row i.  Its four groups take the own results of a warp each, and the
     // prefix's in turn
     const bool mine = r0 + warp < rows;
@@ -867,8 +875,10 @@ ViewPlan view_plan(const ViewDims& d) {
   const double merge = 1.0 + (double)d.n_q * d.H * 64 * 8 / 3.0e6;
   p.rows = p.packed && (long long)d.n_q * d.G <= 4 && (p.small_own || !has_own);
   if (p.rows) {
-    // a block an SM, of 128 keys at least
-    int s = 148 / d.Hk;
+    // two blocks an SM (95 us for a token at 137400 keys of 16 heads, 117 with one);
+    // one where that would leave them few keys, for fewer results to merge
+    int s = 296 / d.Hk;
+    if (d.n_prefix < s * 512) s = 148 / d.Hk;
     if (s > d.n_prefix / 128) s = d.n_prefix / 128;
     p.split_packed = s > 1 ? s : 1;
     p.parts = p.split_packed;
@@ -960,7 +970,7 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
     }
   }
   if (p.small_own) {
-    const dim3 grid((unsigned)d.B, (unsigned)d.Hk);
+    const dim3 grid((unsigned)d.B, (unsigned)d.Hk, (unsigned)ceil_div((long long)d.max_q * d.G, OWN_R));
     if (p.parts > 0)
       return launch_second(view_own_kernel, grid, 32 * OWN_WARPS, st, d, q, ko, vo, p.parts, (const float*)part_o,
                            (const float*)part_lse, out, lse, err);

@@ -38,7 +38,8 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
 
 // How a key_weights call is cut up.
 struct WeightsPlan {
-  int rows;  // at most eight rows: the kernel for those
+  int rows;       // at most eight rows: the kernel for those
+  int own_cores;  // views of few rows: their own keys by CUDA cores
   int prefix_units, own_units;    // work items of 512 keys: of the prefix, of one view at most
   int split_prefix, split_own;    // query ranges of an item
 };
