@@ -21,7 +21,8 @@
 // accounts would queue up at one counter), ranking gives every thread an odd
 // number of consecutive slots (no votes, one scan of the block).  CTAs behind the
 // clusters' copy the accounts and numbers of all slots below n_keep meanwhile;
-// the movers' come over those of the free slots afterwards.
+// the movers' come over those of the free slots afterwards.  The single CTA of few
+// slots does all of it, the moves as well: one launch.
 // move_kernel: copies K and V rows, eight lanes a row.  Bound by memory.
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -35,7 +36,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int BINS = 2048;
-constexpr int kFewSlots = 8192;       // one CTA a head: 9 us against 14 of a cluster at 1705 slots
+constexpr int kFewSlots = 4096;       // one CTA a head: 19 us for 2000 slots of 16 heads against 33 of a cluster and the moves'
 constexpr int kMaxKeys = 96 * 1024;   // sort keys of a slice in shared memory, two bytes each
 constexpr int kCopyCtas = 64;
 
@@ -66,6 +67,9 @@ struct EvictArgs {
   int* n_moves;  // [Hk]
   int* src;      // [Hk][most]
   int* dst;      // [Hk][most]
+  bf16* k;
+  bf16* v;
+  long long k_stride, v_stride;
 };
 
 // Exclusive sum over the threads of the block.
@@ -91,8 +95,35 @@ __device__ __forceinline__ uint32_t threads_before(uint32_t v, uint32_t* scratch
   return __shfl_sync(0xffffffffu, w - own, warp) + sum - v;
 }
 
+// Moves m, m + step, ... of a head (MOVE_UNROLL of them); eight lanes a move.
+constexpr int MOVE_UNROLL = 4;
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int hk, int m, int step, int n) {
+  const int e = (threadIdx.x & 7) * 8;
+  const long long list = (long long)hk * a.most, row = hk * a.w_stride;
+  uint4 kk[MOVE_UNROLL], vv[MOVE_UNROLL];
+  int to[MOVE_UNROLL];
+#pragma unroll
+  for (int u = 0; u < MOVE_UNROLL; ++u, m += step) {
+    to[u] = -1;
+    if (m < n) {
+      const int from = a.src[list + m];
+      to[u] = a.dst[list + m];
+      kk[u] = *reinterpret_cast<const uint4*>(a.k + from * a.k_stride + hk * 64 + e);
+      vv[u] = *reinterpret_cast<const uint4*>(a.v + from * a.v_stride + hk * 64 + e);
+      if (e == 0) a.acc_out[row + to[u]] = a.acc[row + from];
+      if (e == 8) a.ids_out[row + to[u]] = a.ids[row + from];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < MOVE_UNROLL; ++u)
+    if (to[u] >= 0) {
+      *reinterpret_cast<uint4*>(a.k + to[u] * a.k_stride + hk * 64 + e) = kk[u];
+      *reinterpret_cast<uint4*>(a.v + to[u] * a.v_stride + hk * 64 + e) = vv[u];
+    }
+}
+
 template <int CLUSTER, bool IN_SMEM>
-__global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, CLUSTER == 1 ? 1 : 2) select_kernel(const EvictArgs a) {
   extern __shared__ uint16_t s_top[];
   __shared__ Shared sh;
   const int tid = threadIdx.x;
@@ -248,42 +279,30 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const EvictArgs a) 
     const bool stays = kept(slot);
     if (slot < a.keep && !stays) a.dst[list + holes_before++] = slot;
     if (slot >= a.keep && stays) a.src[list + movers_before++] = slot;
+    if (CLUSTER == 1) s_top[slot] = stays;  // the thread's own slots, read for the last time
+  }
+  if (CLUSTER == 1) {
+    __syncthreads();
+    const long long row = hk * a.w_stride;
+    for (int slot = tid; slot < a.keep; slot += kThreads)
+      if (s_top[slot]) {
+        a.acc_out[row + slot] = acc[slot];
+        a.ids_out[row + slot] = ids[slot];
+      }
+    for (int m = tid >> 3; m < (int)all; m += kThreads / 8 * MOVE_UNROLL) move_rows(a, hk, m, kThreads / 8, (int)all);
   }
   sync_all();  // no CTA leaves while another may read its shared memory
 }
 
-constexpr int MOVE_THREADS = 256, MOVE_UNROLL = 4;
+constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_BLOCK = MOVE_THREADS / 8 * MOVE_UNROLL;  // moves of a block
 
-__global__ void __launch_bounds__(MOVE_THREADS)
-    move_kernel(const EvictArgs a, bf16* __restrict__ k, bf16* __restrict__ v, long long k_stride, long long v_stride) {
+__global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictArgs a) {
   // heads vary fastest: equal ranks of all heads lie near one another in memory
-  const int hk = blockIdx.x % a.Hk, e = (threadIdx.x & 7) * 8, grp = threadIdx.x >> 3;
-  const int m0 = blockIdx.x / a.Hk * MOVE_BLOCK;
+  const int hk = blockIdx.x % a.Hk, m0 = blockIdx.x / a.Hk * MOVE_BLOCK;
   pdl_wait();
   const int n = a.n_moves[hk];
-  if (m0 >= n) return;
-  uint4 kk[MOVE_UNROLL], vv[MOVE_UNROLL];
-  int to[MOVE_UNROLL];
-#pragma unroll
-  for (int u = 0; u < MOVE_UNROLL; ++u) {
-    const int m = m0 + u * (MOVE_THREADS / 8) + grp;
-    to[u] = -1;
-    if (m < n) {
-      const int from = a.src[(long long)hk * a.most + m];
-      to[u] = a.dst[(long long)hk * a.most + m];
-      kk[u] = *reinterpret_cast<const uint4*>(k + from * k_stride + hk * 64 + e);
-      vv[u] = *reinterpret_cast<const uint4*>(v + from * v_stride + hk * 64 + e);
-      if (e == 0) a.acc_out[hk * a.w_stride + to[u]] = a.acc[hk * a.w_stride + from];
-      if (e == 8) a.ids_out[hk * a.w_stride + to[u]] = a.ids[hk * a.w_stride + from];
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < MOVE_UNROLL; ++u)
-    if (to[u] >= 0) {
-      *reinterpret_cast<uint4*>(k + to[u] * k_stride + hk * 64 + e) = kk[u];
-      *reinterpret_cast<uint4*>(v + to[u] * v_stride + hk * 64 + e) = vv[u];
-    }
+  if (m0 < n) move_rows(a, hk, m0 + (threadIdx.x >> 3), MOVE_THREADS / 8, n);
 }
 
 int slice_of(int n, int cluster) { return ((n + cluster - 1) / cluster + 31) & ~31; }
@@ -291,9 +310,13 @@ int slice_of(int n, int cluster) { return ((n + cluster - 1) / cluster + 31) & ~
 template <int CLUSTER, bool IN_SMEM>
 cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {
   const size_t smem = IN_SMEM ? (size_t)slice_of(a.n, CLUSTER) * 2 : 0;
-  cudaError_t e = cudaFuncSetAttribute(select_kernel<CLUSTER, IN_SMEM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kMaxKeys * 2);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = allow_smem(select_kernel<CLUSTER, IN_SMEM>, kMaxKeys * 2, &done);
   if (e != cudaSuccess) return e;
+  if (CLUSTER == 1) {
+    select_kernel<CLUSTER, IN_SMEM><<<(unsigned)a.Hk, kThreads, smem, st>>>(a);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.Hk * CLUSTER + kCopyCtas));
   cfg.blockDim = dim3(kThreads);
@@ -305,7 +328,7 @@ cudaError_t launch_select(const EvictArgs& a, cudaStream_t st) {
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = CLUSTER > 1 ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, select_kernel<CLUSTER, IN_SMEM>, a);
 }
 
@@ -328,12 +351,16 @@ cudaError_t launch_cache_evict(const EvictDims& d, bf16* k, bf16* v, const float
   a.n_moves = n_moves;
   a.src = src;
   a.dst = dst;
-  const cudaError_t e = d.n <= kFewSlots               ? launch_select<1, true>(a, st)
-                        : slice_of(d.n, 8) <= kMaxKeys ? launch_select<8, true>(a, st)
-                                                       : launch_select<8, false>(a, st);
+  a.k = k;
+  a.v = v;
+  a.k_stride = d.k_stride;
+  a.v_stride = d.v_stride;
+  if (d.n <= kFewSlots) return launch_select<1, true>(a, st);
+  const cudaError_t e =
+      slice_of(d.n, 8) <= kMaxKeys ? launch_select<8, true>(a, st) : launch_select<8, false>(a, st);
   if (e != cudaSuccess || a.most == 0) return e;
   const long long blocks = (long long)((a.most + MOVE_BLOCK - 1) / MOVE_BLOCK) * d.Hk;
-  return launch_second(move_kernel, dim3((unsigned)blocks), MOVE_THREADS, st, a, k, v, d.k_stride, d.v_stride);
+  return launch_second(move_kernel, dim3((unsigned)blocks), MOVE_THREADS, st, a);
 }
 
 }  // namespace gsa

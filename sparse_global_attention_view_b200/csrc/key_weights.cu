@@ -628,7 +628,8 @@ cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf
   if (items > 0x7fffffffLL - 1024) return cudaErrorInvalidValue;
   a.n_items = (int)items;
   if (a.n_items > 0) {
-    cudaError_t e = cudaFuncSetAttribute(key_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = allow_smem(key_weights_kernel, (int)kSmemBytes, &done);
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mkp, mko;
     auto map = [&](CUtensorMap* m, const bf16* base, int heads, int rows, long long stride, int b1, int b2) {

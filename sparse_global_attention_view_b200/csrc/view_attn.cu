@@ -832,7 +832,8 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
 // host
 
 cudaError_t prepare_kernel() {
-  return cudaFuncSetAttribute(view_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  static std::atomic<unsigned long long> done{0};
+  return allow_smem(view_attn_kernel, (int)kSmemBytes, &done);
 }
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }

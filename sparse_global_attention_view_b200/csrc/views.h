@@ -3,6 +3,8 @@
 // Arguments are validated by the caller.
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace gsa {
@@ -57,6 +59,20 @@ struct EvictDims {
 inline int evict_most_moves(const EvictDims& d) { return d.keep < d.n - d.keep ? d.keep : d.n - d.keep; }
 cudaError_t launch_cache_evict(const EvictDims& d, bf16* k, bf16* v, const float* acc, const int* ids, float* acc_out,
                                int* ids_out, int* n_moves, int* src, int* dst, cudaStream_t st);
+
+// Allows a kernel its dynamic shared memory: once for each device (a microsecond a
+// call otherwise).  `done` belongs to the kernel: a bit for each device.
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes, std::atomic<unsigned long long>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // A second kernel of a call: launched while the first one still runs, so that its
 // start is not waited for.  The first kernel calls pdl_launch() at its start, the

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from functools import cached_property
 
 import torch
 
@@ -40,6 +41,14 @@ class ViewBatch:
                             self.n_own if self.max_own < 0 else self.max_own, int(self.causal), float(self.scale),
                             self.wait_limit_ns, 0, 0, 0, 0, 0, 0)
 
+    @cached_property
+    def _bytes(self) -> bytes:
+        return bytes(self.c())
+
+    def copy_c(self) -> GsaViewBatch:
+        """A structure of its own for one call, which fills in the strides."""
+        return GsaViewBatch.from_buffer_copy(self._bytes)
+
 
 def view_workspace_size(batch: ViewBatch) -> int:
     n = ctypes.c_size_t()
@@ -60,64 +69,71 @@ def new_view_workspace(batch: ViewBatch, device=None, stream=None) -> torch.Tens
     return _new_workspace(view_workspace_size(batch), device, stream)
 
 
-class _Call:
-    """Checks the tensors of one call: all on one device, the right types and layouts."""
+def _workspace(ws) -> tuple[int, int, int]:
+    """Device index, pointer and bytes of a workspace."""
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    n = ws.numel() * ws.element_size()
+    if n < WS_HEADER_BYTES:
+        raise ValueError(f"workspace holds {n} bytes, needs {WS_HEADER_BYTES}")
+    return ws.get_device(), ws.data_ptr(), n
 
-    def __init__(self, ws: torch.Tensor):
-        if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        self.ws = ws
-        self.device = ws.device
-        self.ws_bytes = ws.numel() * ws.element_size()
-        if self.ws_bytes < WS_HEADER_BYTES:
-            raise ValueError(f"workspace holds {self.ws_bytes} bytes, needs {WS_HEADER_BYTES}")
 
-    def _tensor(self, t, dtype, name):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the workspace on {self.device}")
+def _refuse(t, dtype, dev, name, want):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the workspace on cuda:{dev}")
+    raise ValueError(f"{name} must be {want}, got shape {tuple(t.shape)} strides {t.stride()}")
 
-    def rows(self, t, n, heads, dim, name):
-        """Pointer and token stride of [n][heads][dim] bf16 with dense heads; None when n is 0."""
-        if n == 0:
-            return None, 0
-        self._tensor(t, BF16, name)
-        if t.shape != (n, heads, dim):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, dim)}")
-        s = t.stride()
-        if s[2] != 1 or (heads > 1 and s[1] != dim):
-            raise ValueError(f"{name} must have its heads side by side, got strides {s}")
-        return t.data_ptr(), s[0] if n > 1 else 0
 
-    def flat(self, t, dtype, shape, name, optional=False):
-        """Pointer of a contiguous tensor."""
-        if t is None and optional:
-            return None
-        self._tensor(t, dtype, name)
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)} strides {t.stride()}")
+def _rows(t, n, heads, dev, name, exact=True):
+    """Pointer and token stride of bf16 [n][heads][64] whose heads lie side by side; (None, 0) when n is 0.
+
+    With ``exact`` false the tensor may hold more than n tokens."""
+    if n == 0:
+        return None, 0
+    if isinstance(t, torch.Tensor) and t.dtype is BF16 and t.get_device() == dev and t.dim() == 3:
+        tokens, h, dim = t.shape
+        s0, s1, s2 = t.stride()
+        if (tokens == n or (not exact and tokens > n)) and h == heads and dim == 64 and s2 == 1 and (s1 == 64 or h == 1):
+            return t.data_ptr(), s0 if tokens > 1 else 0
+    _refuse(t, BF16, dev, name, f"[{'' if exact else '>= '}{n}, {heads}, 64] with its heads side by side")
+
+
+def _flat(t, dtype, shape, dev, name, optional=False):
+    """Pointer of a contiguous tensor."""
+    if t is None and optional:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
+    _refuse(t, dtype, dev, name, f"contiguous {shape}")
 
-    def table(self, t, dtype, heads, least, name, optional=False):
-        """Pointer and row stride of [heads][>= least] with dense rows."""
-        if t is None and optional:
-            return None, 0
-        self._tensor(t, dtype, name)
-        if t.dim() != 2 or t.shape[0] != heads or t.shape[1] < least or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name} must be [{heads}, >= {least}] with dense rows, got {tuple(t.shape)} strides {t.stride()}")
-        return t.data_ptr(), t.stride(0) if heads > 1 else t.shape[1]
 
-    def run(self, fn, where, stream, *args):
-        if torch.cuda.current_device() == self.device.index:
+def _table(t, dtype, heads, least, dev, name, optional=False):
+    """Pointer and row stride of [heads][>= least] with dense rows."""
+    if t is None and optional:
+        return None, 0
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.dim() == 2:
+        h, n = t.shape
+        s0, s1 = t.stride()
+        if h == heads and n >= least and (s1 == 1 or n <= 1):
+            return t.data_ptr(), s0 if h > 1 else n
+    _refuse(t, dtype, dev, name, f"[{heads}, >= {least}] with dense rows")
+
+
+def _run(fn, where, dev, stream, *args) -> None:
+    if torch.cuda.current_device() == dev:
+        st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
             st = torch.cuda.current_stream() if stream is None else stream
-            check(fn(*args, st.cuda_stream), where)
-        else:
-            with torch.cuda.device(self.device):
-                st = torch.cuda.current_stream() if stream is None else stream
-                check(fn(*args, st.cuda_stream), where)
+            status = fn(*args, st.cuda_stream)
+    if status:
+        check(status, where)
 
 
 def prefix_attn(batch: ViewBatch, q, k_prefix, v_prefix, k_own, v_own, q_off, own_off, out, lse, ws,
@@ -127,18 +143,19 @@ def prefix_attn(batch: ViewBatch, q, k_prefix, v_prefix, k_own, v_own, q_off, ow
     q, out [n_q, H, 64], keys and values [n, Hk, 64] bf16, any token stride that is a multiple of 8;
     q_off, own_off [n_views + 1] int32; lse [n_q, H] float32 or None.  Tensors of no tokens may be None.
     """
-    c, b = _Call(ws), batch.c()
-    D, H, Hk = batch.head_dim, b.n_heads, b.n_kv_heads
-    pq, b.q_stride = c.rows(q, b.n_q, H, D, "q")
-    pkp, b.k_prefix_stride = c.rows(k_prefix, b.n_prefix, Hk, D, "k_prefix")
-    pvp, b.v_prefix_stride = c.rows(v_prefix, b.n_prefix, Hk, D, "v_prefix")
-    pko, b.k_own_stride = c.rows(k_own, b.n_own, Hk, D, "k_own")
-    pvo, b.v_own_stride = c.rows(v_own, b.n_own, Hk, D, "v_own")
-    pout, b.out_stride = c.rows(out, b.n_q, H, D, "out")
+    dev, pws, ws_bytes = _workspace(ws)
+    b = batch.copy_c()
+    n_q, n_prefix, n_own, H, Hk = b.n_q, b.n_prefix, b.n_own, b.n_heads, b.n_kv_heads
+    pq, b.q_stride = _rows(q, n_q, H, dev, "q")
+    pkp, b.k_prefix_stride = _rows(k_prefix, n_prefix, Hk, dev, "k_prefix")
+    pvp, b.v_prefix_stride = _rows(v_prefix, n_prefix, Hk, dev, "v_prefix")
+    pko, b.k_own_stride = _rows(k_own, n_own, Hk, dev, "k_own")
+    pvo, b.v_own_stride = _rows(v_own, n_own, Hk, dev, "v_own")
+    pout, b.out_stride = _rows(out, n_q, H, dev, "out")
     offs = (b.n_views + 1,)
-    c.run(load().prefix_attn, "prefix_attn", stream, ctypes.byref(b), pq, pkp, pvp, pko, pvo,
-          c.flat(q_off, I32, offs, "q_off"), c.flat(own_off, I32, offs, "own_off"), pout,
-          c.flat(lse, F32, (b.n_q, H), "lse", True), ws.data_ptr(), c.ws_bytes)
+    _run(load().prefix_attn, "prefix_attn", dev, stream, ctypes.byref(b), pq, pkp, pvp, pko, pvo,
+         _flat(q_off, I32, offs, dev, "q_off"), _flat(own_off, I32, offs, dev, "own_off"), pout,
+         _flat(lse, F32, (n_q, H), dev, "lse", True), pws, ws_bytes)
 
 
 def key_weights(batch: ViewBatch, q, k_prefix, k_own, q_off, own_off, lse, acc, acc_out, decay: float, ws,
@@ -148,17 +165,18 @@ def key_weights(batch: ViewBatch, q, k_prefix, k_own, q_off, own_off, lse, acc, 
     acc_out [Hk, >= n_prefix + n_own] float32 gets decay * acc + the sums for the cached tokens and the sums for the
     own tokens behind them; acc [Hk, >= n_prefix] may be None (zeros) or acc_out itself.
     """
-    c, b = _Call(ws), batch.c()
-    D, H, Hk = batch.head_dim, b.n_heads, b.n_kv_heads
-    pq, b.q_stride = c.rows(q, b.n_q, H, D, "q")
-    pkp, b.k_prefix_stride = c.rows(k_prefix, b.n_prefix, Hk, D, "k_prefix")
-    pko, b.k_own_stride = c.rows(k_own, b.n_own, Hk, D, "k_own")
+    dev, pws, ws_bytes = _workspace(ws)
+    b = batch.copy_c()
+    n_q, n_prefix, n_own, H, Hk = b.n_q, b.n_prefix, b.n_own, b.n_heads, b.n_kv_heads
+    pq, b.q_stride = _rows(q, n_q, H, dev, "q")
+    pkp, b.k_prefix_stride = _rows(k_prefix, n_prefix, Hk, dev, "k_prefix")
+    pko, b.k_own_stride = _rows(k_own, n_own, Hk, dev, "k_own")
     offs = (b.n_views + 1,)
-    pout, out_stride = c.table(acc_out, F32, Hk, b.n_prefix + b.n_own, "acc_out")
-    pacc, acc_stride = c.table(acc, F32, Hk, b.n_prefix, "acc", True)
-    c.run(load().key_weights, "key_weights", stream, ctypes.byref(b), pq, pkp, pko, c.flat(q_off, I32, offs, "q_off"),
-          c.flat(own_off, I32, offs, "own_off"), c.flat(lse, F32, (b.n_q, H), "lse"), pacc, acc_stride, pout, out_stride,
-          decay, ws.data_ptr(), c.ws_bytes)
+    pout, out_stride = _table(acc_out, F32, Hk, n_prefix + n_own, dev, "acc_out")
+    pacc, acc_stride = _table(acc, F32, Hk, n_prefix, dev, "acc", True)
+    _run(load().key_weights, "key_weights", dev, stream, ctypes.byref(b), pq, pkp, pko,
+         _flat(q_off, I32, offs, dev, "q_off"), _flat(own_off, I32, offs, dev, "own_off"),
+         _flat(lse, F32, (n_q, H), dev, "lse"), pacc, acc_stride, pout, out_stride, decay, pws, ws_bytes)
 
 
 def _cache(n_kv_heads: int, n_tokens: int, n_keep: int, recent_from: int = 0) -> GsaCache:
@@ -185,18 +203,15 @@ def cache_evict(n_tokens: int, n_keep: int, recent_from: int, k, v, acc, ids, ac
     [Hk, >= n_tokens] with one row stride.  Afterwards the first n_keep slots of k, v, acc_out and ids_out are the cache.
     Tokens whose number is recent_from or more rank first.
     """
-    c = _Call(ws)
-    for t, name in ((k, "k"), (v, "v")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[0] < n_tokens:
-            raise ValueError(f"{name} must be [>= {n_tokens}, heads, 64]")
-    Hk = k.shape[1]
-    b = _cache(Hk, n_tokens, n_keep, recent_from)
-    pk, b.k_stride = c.rows(k[:n_tokens], n_tokens, Hk, 64, "k")
-    pv, b.v_stride = c.rows(v[:n_tokens], n_tokens, Hk, 64, "v")
-    tables = [c.table(t, dt, Hk, n_tokens, name) for t, dt, name in
-              ((acc, F32, "acc"), (ids, I32, "ids"), (acc_out, F32, "acc_out"), (ids_out, I32, "ids_out"))]
-    if len({s for _, s in tables}) != 1:
-        raise ValueError(f"acc, ids, acc_out and ids_out must have one row stride, got {[s for _, s in tables]}")
-    b.w_stride = tables[0][1]
-    c.run(load().cache_evict, "cache_evict", stream, ctypes.byref(b), pk, pv, *[p for p, _ in tables], ws.data_ptr(),
-          c.ws_bytes)
+    dev, pws, ws_bytes = _workspace(ws)
+    Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+    pk, k_stride = _rows(k, n_tokens, Hk, dev, "k", False)
+    pv, v_stride = _rows(v, n_tokens, Hk, dev, "v", False)
+    pa, stride = _table(acc, F32, Hk, n_tokens, dev, "acc")
+    pi, s1 = _table(ids, I32, Hk, n_tokens, dev, "ids")
+    pao, s2 = _table(acc_out, F32, Hk, n_tokens, dev, "acc_out")
+    pio, s3 = _table(ids_out, I32, Hk, n_tokens, dev, "ids_out")
+    if Hk > 1 and not stride == s1 == s2 == s3:
+        raise ValueError(f"acc, ids, acc_out and ids_out must have one row stride, got {(stride, s1, s2, s3)}")
+    b = GsaCache(Hk, 64, n_tokens, n_keep, recent_from, k_stride, v_stride, stride)
+    _run(load().cache_evict, "cache_evict", dev, stream, ctypes.byref(b), pk, pv, pa, pi, pao, pio, pws, ws_bytes)
