@@ -34,6 +34,7 @@ from .api import (  # noqa: F401
 )
 from .views import (  # noqa: F401
     ViewBatch,
+    ViewCache,
     cache_evict,
     cache_workspace_size,
     key_weights,

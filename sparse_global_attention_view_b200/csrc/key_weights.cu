@@ -580,7 +580,7 @@ WeightsPlan weights_plan(const ViewDims& d) {
   if (own_items > d.n_own / ITEM + d.B) own_items = d.n_own / ITEM + d.B;
   double best = 0;
   for (int s = 1; s <= 32 && s <= (tiles_p > 1 ? tiles_p : 1); ++s) {
-    const int per_p = ceil_div(tiles_p, s), so = per_p > 0 ? ceil_div(tiles_o, per_p) : 1;
+    const int per_p = ceil_div(tiles_p, s), so = per_p > 0 && tiles_o > 0 ? ceil_div(tiles_o, per_p) : 1;
     const double items = ((double)p.prefix_units * s + (double)own_items * so) * d.Hk;
     const double work = ((double)p.prefix_units * s * (per_p + 2.0) + (double)own_items * so * (ceil_div(tiles_o, so) + 2.0)) * d.Hk;
     const double longest = (per_p > ceil_div(tiles_o, so) ? per_p : ceil_div(tiles_o, so)) + 2.0;
@@ -588,7 +588,7 @@ WeightsPlan weights_plan(const ViewDims& d) {
     if (s == 1 || cost < best) {
       best = cost;
       p.split_prefix = s;
-      p.split_own = so > 1 ? so : 1;
+      p.split_own = so;
     }
   }
   return p;

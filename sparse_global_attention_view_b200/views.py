@@ -15,7 +15,7 @@ from functools import cached_property
 import torch
 
 from ._lib import GsaCache, GsaViewBatch, check, load
-from .api import BF16, F32, I32, WS_HEADER_BYTES
+from .api import BF16, F32, I32, WS_HEADER_BYTES, check_device_error
 
 
 @dataclass(frozen=True)
@@ -215,3 +215,72 @@ def cache_evict(n_tokens: int, n_keep: int, recent_from: int, k, v, acc, ids, ac
         raise ValueError(f"acc, ids, acc_out and ids_out must have one row stride, got {(stride, s1, s2, s3)}")
     b = GsaCache(Hk, 64, n_tokens, n_keep, recent_from, k_stride, v_stride, stride)
     _run(load().cache_evict, "cache_evict", dev, stream, ctypes.byref(b), pk, pv, pa, pi, pao, pio, pws, ws_bytes)
+
+
+class ViewCache:
+    """Keys and values of the views seen so far, with their account: the operators in the order of a stream of views.
+
+    ``step`` attends a batch of views to the cache and to their own tokens, adds up who was looked at and appends the
+    tokens; ``evict`` shrinks the cache.  Everything runs on the current stream of ``device``.
+    """
+
+    def __init__(self, capacity: int, n_heads: int, n_kv_heads: int = 0, device="cuda", scale: float = 0.0):
+        self.capacity, self.n_heads, self.n_kv_heads, self.scale = capacity, n_heads, n_kv_heads or n_heads, scale
+        self.k = torch.empty(capacity, self.n_kv_heads, 64, dtype=BF16, device=device)
+        self.v = torch.empty_like(self.k)
+        # accounts and token numbers, and where the next call leaves them
+        self.acc = torch.zeros(self.n_kv_heads, capacity, dtype=F32, device=device)
+        self.ids = torch.zeros(self.n_kv_heads, capacity, dtype=I32, device=device)
+        self._acc, self._ids = torch.zeros_like(self.acc), torch.zeros_like(self.ids)
+        self.n = 0        # tokens in the cache
+        self.next_id = 0  # tokens ever appended
+        self._ws = None
+
+    def _workspace(self, n_bytes: int) -> torch.Tensor:
+        if self._ws is None or self._ws.numel() < n_bytes:
+            self._ws = _new_workspace(n_bytes, self.k.device, None)
+        return self._ws
+
+    def step(self, q, k, v, lens=None, decay: float = 1.0) -> torch.Tensor:
+        """Attention of the views (``lens`` tokens each; all of them one view by default) to the cache and to their
+        own tokens, q [n, H, 64], k and v [n, Hk, 64]; then the tokens join the cache."""
+        n = q.shape[0]
+        lens = [n] if lens is None else list(lens)
+        if sum(lens) != n:
+            raise ValueError(f"the views have {sum(lens)} tokens, q has {n}")
+        if self.n + n > self.capacity:
+            raise ValueError(f"{self.n} + {n} tokens do not fit a cache of {self.capacity}")
+        at = [0]
+        for x in lens:
+            at.append(at[-1] + x)
+        off = torch.tensor(at, dtype=I32, device=self.k.device)
+        batch = ViewBatch(n_views=len(lens), n_q=n, n_own=n, n_prefix=self.n, n_heads=self.n_heads,
+                          n_kv_heads=self.n_kv_heads, max_q=max(lens), max_own=max(lens), scale=self.scale)
+        ws = self._workspace(view_workspace_size(batch))
+        out = torch.empty(n, self.n_heads, 64, dtype=BF16, device=self.k.device)
+        lse = torch.empty(n, self.n_heads, dtype=F32, device=self.k.device)
+        kp, vp = self.k[:self.n], self.v[:self.n]
+        prefix_attn(batch, q, kp, vp, k, v, off, off, out, lse, ws)
+        key_weights(batch, q, kp, k, off, off, lse, self.acc, self.acc, decay, ws)
+        self.k[self.n:self.n + n].copy_(k)
+        self.v[self.n:self.n + n].copy_(v)
+        self.ids[:, self.n:self.n + n] = torch.arange(self.next_id, self.next_id + n, dtype=I32, device=self.k.device)
+        self.n += n
+        self.next_id += n
+        return out
+
+    def evict(self, n_keep: int, recent: int = 0) -> None:
+        """Keeps ``n_keep`` tokens a head: the ``recent`` newest, then those with the largest account."""
+        if n_keep >= self.n:
+            return
+        ws = self._workspace(cache_workspace_size(self.n_kv_heads, self.n, n_keep))
+        cache_evict(self.n, n_keep, self.next_id - recent, self.k, self.v, self.acc, self.ids, self._acc, self._ids, ws)
+        self.acc, self._acc = self._acc, self.acc
+        self.ids, self._ids = self._ids, self.ids
+        self.n = n_keep
+
+    def check_device_error(self) -> None:
+        """Raises if a kernel of an earlier call reported an error (synchronises)."""
+        if self._ws is not None:
+            with torch.cuda.device(self.k.device):
+                check_device_error(self._ws)

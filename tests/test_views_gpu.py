@@ -210,3 +210,395 @@ def test_evict_twice_is_evict_once():
     k, v, acc, ids = cache(2, 3000, 2)
     k2, v2, acc2, ids2 = evict(k, v, acc, ids, 1700, 2900)
     assert_evicted(k, v, acc, ids, 1700, 2900, *evict(k2, v2, acc, ids, 1700, 2900))
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# how users hold their tensors
+
+# a shape for each way a call is cut up: one row, few rows, packed rows with the own keys apart, long views
+WAYS = {
+    "one token": (2, 2, [1], [9], 700),
+    "poses": (4, 2, [1, 5, 3, 2], [0, 100, 31, 7], 700),
+    "mixed views": (2, 2, [1, 300, 2], [50, 300, 200], 300),
+    "long views": (2, 2, [300, 280], [300, 280], 300),
+}
+
+
+def everything(x, causal=False, decay=0.75, **kw):
+    """attend and weigh, against their formulas."""
+    batch = batch_of(x, causal, **kw)
+    out, lse = attend(x, batch)
+    assert_attend(x, out, lse, causal)
+    lse = exact_lse(x, causal)
+    acc = torch.rand(x["kp"].shape[1], x["kp"].shape[0], device=DEV)
+    assert_weights(x, weigh(x, batch, lse, acc, decay), lse, acc, decay, causal)
+
+
+@pytest.mark.parametrize("name", list(WAYS))
+def test_slices_of_larger_tensors(name):
+    x = make(*WAYS[name])
+    H, Hk = x["q"].shape[1], x["kp"].shape[1]
+    nq, nt, P = x["q"].shape[0], x["ko"].shape[0], x["kp"].shape[0]
+    fused = torch.full((nq, H + 2, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    fused[:, 1:1 + H] = x["q"]
+    kv = torch.full((P + 100, 2, Hk, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    kv[:P, 0], kv[:P, 1] = x["kp"], x["vp"]
+    own = torch.full((nt, 3 * Hk, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    own[:, Hk:2 * Hk], own[:, 2 * Hk:] = x["ko"], x["vo"]
+    x.update(q=fused[:, 1:1 + H], kp=kv[:P, 0], vp=kv[:P, 1], ko=own[:, Hk:2 * Hk], vo=own[:, 2 * Hk:])
+    everything(x)
+    # an output of a larger tensor: what lies around it stays
+    room = torch.full((nq, H + 1, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    out, lse = attend(x, batch_of(x), room[:, :H])
+    assert_attend(x, out, lse)
+    assert (room[:, H] == 7).all()
+    # an account with longer rows, in place
+    acc = torch.full((Hk, P + nt + 13), 7.0, device=DEV)
+    acc[:, :P] = torch.rand(Hk, P, device=DEV)
+    before, z = acc.clone(), exact_lse(x)
+    weigh(x, batch_of(x), z, acc, 0.5, acc)
+    assert_weights(x, acc, z, before, 0.5)
+    assert (acc[:, P + nt:] == 7).all()
+
+
+@pytest.mark.parametrize("name", list(WAYS))
+def test_rows_of_no_view(name):
+    x = make(*WAYS[name])
+    nan = float("nan")
+
+    def padded(t, front, back):
+        pad = lambda n: torch.full((n, *t.shape[1:]), nan, dtype=t.dtype, device=DEV)  # noqa: E731
+        return torch.cat((pad(front), t, pad(back)))
+
+    nq, nt = x["q"].shape[0], x["ko"].shape[0]
+    x.update(q=padded(x["q"], 3, 150), ko=padded(x["ko"], 5, 140), vo=padded(x["vo"], 5, 140),
+             q_off=[3 + a for a in x["q_off"]], own_off=[5 + a for a in x["own_off"]])
+    batch = batch_of(x)
+    out, lse = attend(x, batch)
+    assert_attend(x, out, lse)
+    z = exact_lse(x)
+    got = weigh(x, batch, z, None, 1.0)
+    assert_weights(x, got, z, None, 1.0)
+    for rows in (slice(0, 3), slice(3 + nq, None)):
+        assert (out[rows] == 7).all() and (lse[rows] == 7).all()
+    P = x["kp"].shape[0]
+    assert (got[:, P:P + 5] == 7).all() and (got[:, P + 5 + nt:] == 7).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("name", ["poses", "mixed views", "long views"])
+def test_bad_values_stay_in_their_view(name, bad):
+    x = make(*WAYS[name])
+    batch, z = batch_of(x), exact_lse(x)
+    good = attend(x, batch)
+    w = weigh(x, batch, z, None, 1.0)
+    x["ko"], x["vo"] = x["ko"].clone(), x["vo"].clone()
+    rows, cols = slice(x["q_off"][1], x["q_off"][2]), slice(x["own_off"][1], x["own_off"][2])
+    x["ko"][cols], x["vo"][cols] = bad, bad
+    out, lse = attend(x, batch)
+    # view 1 sees keys without a finite score: a score of +inf or NaN leaves no number (one of -inf would, but the
+    # queries' signs give both)
+    assert out[rows].isnan().all() and lse[rows].isnan().all()
+    keep = torch.ones(out.shape[0], dtype=torch.bool)
+    keep[rows] = False
+    assert torch.equal(out[keep], good[0][keep]) and torch.equal(lse[keep], good[1][keep])
+    w2 = weigh(x, batch, z, None, 1.0)
+    P = x["kp"].shape[0]
+    keep = torch.ones(w.shape[1], dtype=torch.bool)
+    keep[P + cols.start:P + cols.stop] = False
+    assert torch.equal(w2[:, keep], w[:, keep])
+
+
+@pytest.mark.parametrize("name", list(WAYS))
+def test_a_nan_that_is_seen_shows(name):
+    for j in (0, 77, 299):
+        x = make(*WAYS[name])
+        x["kp"][j, 0] = float("nan")
+        out, lse = attend(x, batch_of(x))
+        G_ = x["q"].shape[1] // x["kp"].shape[1]
+        assert out[:, :G_].isnan().all() and lse[:, :G_].isnan().all()
+        assert not out[:, G_:].isnan().any()
+
+
+@pytest.mark.parametrize("strength", [0.0, 30.0, 3000.0])
+@pytest.mark.parametrize("name", list(WAYS))
+def test_flat_and_steep_scores(name, strength):
+    x = make(*WAYS[name], strength=strength)
+    out, lse = attend(x, batch_of(x))
+    assert_attend(x, out, lse)
+    if strength <= 30:
+        z = exact_lse(x)
+        assert_weights(x, weigh(x, batch_of(x), z, None, 1.0), z, None, 1.0)
+
+
+@pytest.mark.parametrize("name", list(WAYS))
+def test_scale(name):
+    x = make(*WAYS[name])
+    out, lse = attend(x, batch_of(x, scale=0.5))
+    assert_attend(x, out, lse, scale=0.5)
+
+
+@pytest.mark.parametrize("name", list(WAYS))
+def test_rising_scores_rescale(name):
+    # every key tile raises the maximum by far
+    x = make(*WAYS[name])
+    n = x["kp"].shape[0]
+    ramp = torch.linspace(0.1, 40, n, device=DEV)[:, None, None]
+    x["q"] = x["q"].abs()
+    x["kp"] = (x["kp"].abs() * ramp).bfloat16()
+    out, lse = attend(x, batch_of(x))
+    assert_attend(x, out, lse)
+
+
+def test_a_cache_beyond_4_gigabytes():
+    # token strides that take offsets past 2^32 bytes
+    n, stride = 40_000, 1 << 16
+    room = torch.empty(n * stride, dtype=torch.bfloat16, device=DEV)
+    for ql in ([1], [1, 2, 3, 4], [300]):
+        x = make(2, 2, ql, [3] * len(ql), 8)
+        g = torch.Generator(device=DEV).manual_seed(1)
+        k = room.as_strided((n, 2, 64), (stride, 64, 1))
+        v = room.as_strided((n, 2, 64), (stride, 64, 1), 128)
+        k.copy_(torch.randn(n, 2, 64, generator=g, device=DEV))
+        v.copy_(torch.randn(n, 2, 64, generator=g, device=DEV))
+        x.update(kp=k, vp=v)
+        out, lse = attend(x, batch_of(x))
+        assert_attend(x, out, lse)
+        z = exact_lse(x)
+        assert_weights(x, weigh(x, batch_of(x), z, None, 1.0), z, None, 1.0)
+    _, _, acc, ids = cache(2, n, 3)
+    k0, v0 = k.clone(), v.clone()
+    acc2, ids2 = torch.empty_like(acc), torch.empty_like(ids)
+    G().cache_evict(n, 30_000, n, k, v, acc, ids, acc2, ids2, G().new_cache_workspace(2, n, 30_000))
+    assert_evicted(k0, v0, acc, ids, 30_000, n, k, v, acc2, ids2)
+
+
+@pytest.mark.parametrize("n", [1705, 6000])
+def test_evict_slices_of_larger_tensors(n):
+    k, v, acc, ids = cache(3, n, 8)
+    kv = torch.full((n + 9, 2, 3, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    kv[:n, 0], kv[:n, 1] = k, v
+    wide = [torch.full((3, n + 77), 7, dtype=t.dtype, device=DEV) for t in (acc, ids, acc, ids)]
+    wide[0][:, :n], wide[1][:, :n] = acc, ids
+    keep, recent_from = n - 400, n - 100
+    G().cache_evict(n, keep, recent_from, kv[:, 0], kv[:, 1], *wide, G().new_cache_workspace(3, n, keep))
+    assert_evicted(k, v, acc, ids, keep, recent_from, kv[:n, 0], kv[:n, 1], wide[2], wide[3])
+    assert (kv[n:] == 7).all() and (wide[2][:, keep:] == 7).all() and (wide[3][:, keep:] == 7).all()
+
+
+@pytest.mark.parametrize("n", [1000, 9000])
+def test_evict_nothing_and_everything(n):
+    k, v, acc, ids = cache(2, n, 4)
+    assert_evicted(k, v, acc, ids, n, n, *evict(k, v, acc, ids, n, n))
+    k2, v2, acc2, ids2 = evict(k, v, acc, ids, 0, n)
+    assert torch.equal(k2, k) and torch.equal(v2, v)
+
+
+def test_account_of_special_values():
+    x = make(2, 2, [20], [20], 300)
+    z = exact_lse(x)
+    w = weigh(x, batch_of(x), z, None, 1.0)
+    acc = torch.full((2, 300), float("nan"), device=DEV)
+    assert torch.equal(weigh(x, batch_of(x), z, acc, 0.0), w)  # not read
+    acc[:] = float("inf")
+    got = weigh(x, batch_of(x), z, acc, 0.5)
+    assert (got[:, :300] == float("inf")).all() and torch.equal(got[:, 300:], w[:, 300:])
+    z[3] = float("-inf")  # a query that counts for nothing
+    y = dict(x, q=x["q"].clone())
+    y["q"][3] = 0
+    z2 = z.clone()
+    z2[3] = 1000.0
+    assert torch.allclose(weigh(x, batch_of(x), z, None, 1.0), weigh(y, batch_of(y), z2, None, 1.0), rtol=1e-6)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# streams, graphs, errors
+
+
+@pytest.mark.parametrize("name", list(WAYS) + ["split rows"])
+def test_equal_calls_give_equal_bits(name):
+    x = make(*(WAYS | SIZES)[name])
+    batch = batch_of(x)
+    a, b = attend(x, batch), attend(x, batch)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    z = exact_lse(x)
+    assert torch.equal(weigh(x, batch, z, None, 1.0), weigh(x, batch, z, None, 1.0))
+
+
+def test_another_stream():
+    side = torch.cuda.Stream()
+    x = make(*WAYS["mixed views"])
+    k, v, acc, ids = cache(2, 5000, 6)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)  # what runs on the wrong stream would be early
+        y = {n: (t.clone() if isinstance(t, torch.Tensor) else t) for n, t in x.items()}
+        batch = batch_of(y)
+        out, lse = attend(y, batch)
+        w = weigh(y, batch, lse, None, 1.0)
+        moved = evict(k, v, acc, ids, 3000, 4900)
+    side.synchronize()
+    # the stream as an argument
+    ws = G().new_view_workspace(batch, stream=side)
+    out2 = torch.zeros_like(out)
+    lse2 = torch.zeros_like(lse)
+    torch.cuda.synchronize()
+    G().prefix_attn(batch, y["q"], y["kp"], y["vp"], y["ko"], y["vo"], ints(y["q_off"]), ints(y["own_off"]), out2, lse2, ws,
+                    side)
+    side.synchronize()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert_attend(x, out, lse)
+    assert_weights(x, w, lse, None, 1.0)
+    assert_evicted(k, v, acc, ids, 3000, 4900, *moved)
+
+
+@pytest.mark.parametrize("name", list(WAYS))
+def test_captured_calls(name):
+    x = make(*WAYS[name])
+    batch = batch_of(x, max_q=x["q"].shape[0], max_own=x["ko"].shape[0])
+    P, nt = x["kp"].shape[0], x["ko"].shape[0]
+    Hk = x["kp"].shape[1]
+    ws, q_off, own_off = G().new_view_workspace(batch), ints(x["q_off"]), ints(x["own_off"])
+    out = torch.full(x["q"].shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(x["q"].shape[:2], 7.0, device=DEV)
+    acc, acc_out = torch.rand(Hk, P + nt, device=DEV), torch.full((Hk, P + nt), 7.0, device=DEV)
+    k, v, ids = x["kp"].clone(), x["vp"].clone(), torch.arange(P, dtype=torch.int32, device=DEV).repeat(Hk, 1)
+    keep, wide = P - 100, torch.full((Hk, P), 7.0, device=DEV)
+    ids2, evict_ws = torch.zeros_like(ids), G().new_cache_workspace(Hk, P, P - 100)
+
+    def calls():
+        G().prefix_attn(batch, x["q"], x["kp"], x["vp"], x["ko"], x["vo"], q_off, own_off, out, lse, ws)
+        G().key_weights(batch, x["q"], x["kp"], x["ko"], q_off, own_off, lse, acc, acc_out, 0.5, ws)
+        G().cache_evict(P, keep, P, k, v, acc_out[:, :P].clone(), ids, wide, ids2, evict_ws)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        calls()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    # other inputs, and other views in the same buffers
+    y = make(*WAYS[name], seed=9)
+    if len(y["q_off"]) > 2:
+        y["q_off"][1] -= min(1, y["q_off"][1])
+        y["own_off"][-1] -= 3
+    for n in ("q", "kp", "vp", "ko", "vo"):
+        x[n].copy_(y[n])
+    q_off.copy_(ints(y["q_off"]))
+    own_off.copy_(ints(y["own_off"]))
+    k.copy_(y["kp"])
+    v.copy_(y["vp"])
+    out.fill_(7)
+    lse.fill_(7)
+    acc_out.fill_(7)
+    graph.replay()
+    torch.cuda.synchronize()
+    G().check_device_error(ws)
+    assert_attend(y, out, lse)
+    assert_weights(y, acc_out, lse, acc[:, :P], 0.5)
+    assert_evicted(y["kp"], y["vp"], acc_out[:, :P], ids, keep, P, k, v, wide, ids2)
+
+
+@pytest.mark.parametrize("name", list(WAYS))
+def test_bad_offsets_are_reported(name):
+    x = make(*WAYS[name])
+    batch = batch_of(x)
+    good = attend(x, batch)
+    z = exact_lse(x)
+    nq, nt, B = x["q"].shape[0], x["ko"].shape[0], len(x["q_off"]) - 1
+    cases = [dict(own_off=x["own_off"][:-1] + [nt + 1]), dict(own_off=[-1] + x["own_off"][1:]),
+             dict(q_off=x["q_off"][:-1] + [nq + 7])]
+    if B > 1:
+        cases += [dict(q_off=[0, nq] + [0] * (B - 1)), dict(own_off=[0] * B + [nt])]
+    for case in cases:
+        for call in (lambda y: attend(y, batch), lambda y: weigh(y, batch, z, None, 1.0)):
+            with pytest.raises(G().GsaError) as e:
+                call(x | case)
+            assert e.value.status == 6, case
+    again = attend(x, batch)
+    assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+
+
+def test_waits_that_run_out():
+    # the hardware itself holds a waiting thread for a microsecond or so before the limit is looked at, so this takes
+    # waits that are longer: the copies' on a full ring of key or query tiles
+    x = make(2, 2, [3000], [10], 6000)
+    batch, z = batch_of(x), exact_lse(x)
+    short = batch_of(x, wait_limit_ns=1)
+    for call in (lambda b: attend(x, b), lambda b: weigh(x, b, z, None, 1.0)):
+        with pytest.raises(G().GsaError) as e:
+            call(short)
+        assert e.value.status == 5
+    out, lse = attend(x, batch)
+    assert_attend(x, out, lse)
+    assert_weights(x, weigh(x, batch, z, None, 1.0), z, None, 1.0)
+
+
+def test_python_refusals():
+    x = make(2, 2, [5], [5], 300)
+    batch = batch_of(x)
+    ws, off = G().new_view_workspace(batch), ints([0, 5])
+    out, lse = torch.empty_like(x["q"]), torch.empty(5, 2, device=DEV)
+    args = [x["q"], x["kp"], x["vp"], x["ko"], x["vo"], off, off, out, lse, ws]
+    for i, bad in ((0, x["q"].float()), (0, x["q"][:4]), (0, x["q"].cpu()), (0, None), (1, x["kp"][:, :, ::2]), (2, x["vp"][:, :1]),
+                   (3, x["ko"].transpose(0, 1)), (5, off.long()), (5, ints([0, 5, 5])), (8, lse[:, :1]), (8, lse.double()),
+                   (9, ws[:100]), (9, ws.cpu())):
+        with pytest.raises(ValueError):
+            G().prefix_attn(batch, *args[:i], bad, *args[i + 1:])
+    with pytest.raises(G().GsaError) as e:  # two bytes off
+        G().prefix_attn(batch, torch.empty(5 * 128 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(5, 2, 64), *args[1:])
+    assert e.value.status == 1
+    big = batch_of(make(2, 2, [300], [10], 6000))
+    y = make(2, 2, [300], [10], 6000)
+    with pytest.raises(G().GsaError) as e:
+        G().prefix_attn(big, y["q"], y["kp"], y["vp"], y["ko"], y["vo"], ints([0, 300]), ints([0, 10]), torch.empty_like(y["q"]),
+                        None, G().new_workspace(None))
+    assert e.value.status == 3
+    k, v, acc, ids = cache(2, 100, 1)
+    evict_ws = G().new_cache_workspace(2, 100, 50)
+    for bad in ((k, v, acc, ids, acc, torch.empty_like(ids)), (k, v, acc, ids, torch.empty_like(acc), ids)):
+        with pytest.raises(G().GsaError):
+            G().cache_evict(100, 50, 100, *bad, evict_ws)
+    with pytest.raises(ValueError):
+        G().cache_evict(101, 50, 100, k, v, acc, ids, torch.empty_like(acc), torch.empty_like(ids), evict_ws)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# a stream of views
+
+
+@pytest.mark.parametrize("H,Hk", [(4, 4), (6, 2)])
+def test_a_stream_of_views(H, Hk):
+    c = G().ViewCache(700, H, Hk)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    seen_k, seen_v = [], []  # every token ever appended
+    acc = torch.zeros(Hk, 0, dtype=torch.float64, device=DEV)
+    heads = torch.arange(Hk, device=DEV)
+    for step, lens in enumerate(([60], [1], [40, 3, 120], [130], [2, 2], [200], [90])):
+        n = sum(lens)
+        q, k, v = (torch.randn(n, h, 64, generator=g, device=DEV).bfloat16() for h in (H, Hk, Hk))
+        kp, vp, ids = c.k[:c.n].clone(), c.v[:c.n].clone(), c.ids[:, :c.n].clone()
+        if c.n:
+            # the cache holds the tokens that its numbers say
+            assert torch.equal(kp, torch.cat(seen_k)[ids.T.long(), heads]) and torch.equal(vp, torch.cat(seen_v)[ids.T.long(), heads])
+        before = c.acc[:, :c.n].clone()
+        out = c.step(q, k, v, lens, decay=0.5)
+        c.check_device_error()
+        off = offsets(lens)
+        o, z, to, _ = R.attend(q, kp, vp, k, v, off, off)
+        assert ((out.double() - o).abs() <= to).all(), step
+        w, tol = R.weights(q, kp, k, off, off, z.float(), before, 0.5)
+        # the account goes by the kernel's own log sums: their error comes on top
+        assert ((c.acc[:, :c.n].double() - w).abs() <= tol + 2e-5 * w).all(), step
+        seen_k.append(k)
+        seen_v.append(v)
+        assert c.n == kp.shape[0] + n and torch.equal(c.ids[:, c.n - n:c.n], c.ids[:1, c.n - n:c.n].expand(Hk, n))
+        if c.n > 300:
+            ids, acc, full = c.ids[:, :c.n].clone(), c.acc[:, :c.n].clone(), c.next_id
+            c.evict(300, recent=50)
+            src = R.evict(acc.cpu(), ids.cpu(), 300, full - 50).to(DEV)
+            assert c.n == 300 and torch.equal(c.ids[:, :300], ids[heads[:, None], src])
+            assert all((c.ids[:, :300] == i).any(1).all() for i in range(full - 50, full))
+    with pytest.raises(ValueError):
+        c.step(*(torch.zeros(500, h, 64, dtype=torch.bfloat16, device=DEV) for h in (H, Hk, Hk)))
