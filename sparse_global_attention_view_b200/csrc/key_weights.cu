@@ -508,16 +508,19 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// Blocks small enough (4096 registers) to run beside a CTA of key_weights_kernel.
+constexpr int OWN_THREADS = 128;
+
 // Own keys of views of few rows: a group of eight lanes takes a key and goes over
 // the queries of its view.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(OWN_THREADS)
     key_weights_own_kernel(const WeightsArgs a, const bf16* __restrict__ q, const bf16* __restrict__ k) {
   const ViewDims& d = a.d;
   const int hk = blockIdx.y, e = (threadIdx.x & 7) * 8;
-  const int j = blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int j = blockIdx.x * (OWN_THREADS / 8) + (threadIdx.x >> 3);
   if (blockIdx.x == 0 && hk == 0) {
     ViewRange r;
-    for (int b = threadIdx.x; b < d.B; b += 256) view_range(d, b, &r, a.err);
+    for (int b = threadIdx.x; b < d.B; b += OWN_THREADS) view_range(d, b, &r, a.err);
   }
   const bool in = j < d.n_own && j >= d.own_off[0] && j < d.own_off[d.B];
   // the view of the key: the last one that starts at or before it
@@ -653,10 +656,10 @@ cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf
     if (e != cudaSuccess) return e;
   }
   if (p.own_cores && d.n_own > 0) {
-    const dim3 grid((unsigned)ceil_div(d.n_own, 32), (unsigned)d.Hk);
+    const dim3 grid((unsigned)ceil_div(d.n_own, OWN_THREADS / 8), (unsigned)d.Hk);
     if (a.n_items > 0 && p.split_prefix == 1)
-      return launch_second(key_weights_own_kernel, grid, 256, st, a, q, ko);
-    key_weights_own_kernel<<<grid, 256, 0, st>>>(a, q, ko);
+      return launch_second(key_weights_own_kernel, grid, OWN_THREADS, st, a, q, ko);
+    key_weights_own_kernel<<<grid, OWN_THREADS, 0, st>>>(a, q, ko);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
