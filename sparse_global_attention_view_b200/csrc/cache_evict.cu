@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t threads_before(uint32_t v, uint32_t* scratch
 }
 
 // Moves m, m + step, ... of a head (MOVE_UNROLL of them); eight lanes a move.
-constexpr int MOVE_UNROLL = 4;
+constexpr int MOVE_UNROLL = 2;
 __device__ __forceinline__ void move_rows(const EvictArgs& a, int hk, int m, int step, int n) {
   const int e = (threadIdx.x & 7) * 8;
   const long long list = (long long)hk * a.most, row = hk * a.w_stride;
@@ -236,27 +236,25 @@ __global__ void __launch_bounds__(kThreads, CLUSTER == 1 ? 1 : 2) select_kernel(
     const uint32_t k = key_of(slot);
     return k > limit ? 2 : (k == limit ? 1 : 0);
   };
+  // kept for certain, and equal to the limit, before and behind `keep`
+  uint32_t more_low = 0, more_high = 0, eq_low = 0, eq_high = 0, total;
+  for (int slot = t0; slot < t1; ++slot) {
+    const int x = rank_of(slot);
+    const bool low = slot < a.keep;
+    more_low += low && x == 2;
+    more_high += !low && x == 2;
+    eq_low += low && x == 1;
+    eq_high += !low && x == 1;
+  }
   // equal keys before the thread's part: in the CTA, then in the cluster
-  uint32_t eq = 0, total;
-  for (int slot = t0; slot < t1; ++slot) eq += rank_of(slot) == 1;
-  uint32_t eq_before = threads_before(eq, sh.warp_sum, &total);
+  uint32_t eq_before = threads_before(eq_low + eq_high, sh.warp_sum, &total);
   if (tid == 0) sh.tot[0] = total;
   sync_all();
   for (int r = 0; r < rank; ++r) eq_before += of_rank(sh.tot, r)[0];
-
   // free slots below `keep`, and kept tokens at or behind it
-  uint32_t holes = 0, movers = 0, run = eq_before;
-  auto kept = [&](int slot) -> bool {
-    const int x = rank_of(slot);
-    const bool stays = x == 2 || (x == 1 && run < want);
-    run += x == 1;
-    return stays;
-  };
-  for (int slot = t0; slot < t1; ++slot) {
-    const bool stays = kept(slot);
-    holes += slot < a.keep && !stays;
-    movers += slot >= a.keep && stays;
-  }
+  const uint32_t left = want > eq_before ? want - eq_before : 0;
+  const uint32_t stay_low = min(left, eq_low), stay_high = min(left - stay_low, eq_high);
+  const uint32_t holes = (uint32_t)max(0, min(t1, a.keep) - t0) - more_low - stay_low, movers = more_high + stay_high;
   uint32_t holes_before = threads_before(holes, sh.warp_sum, &total);
   if (tid == 0) sh.tot[1] = total;
   uint32_t movers_before = threads_before(movers, sh.warp_sum, &total);
@@ -273,13 +271,36 @@ __global__ void __launch_bounds__(kThreads, CLUSTER == 1 ? 1 : 2) select_kernel(
     all += t[2];
   }
   if (rank == 0 && tid == 0) a.n_moves[hk] = (int)all;
-  run = eq_before;
   const long long list = (long long)hk * a.most;
+  uint32_t run = eq_before;
   for (int slot = t0; slot < t1; ++slot) {
-    const bool stays = kept(slot);
-    if (slot < a.keep && !stays) a.dst[list + holes_before++] = slot;
-    if (slot >= a.keep && stays) a.src[list + movers_before++] = slot;
-    if (CLUSTER == 1) s_top[slot] = stays;  // the thread's own slots, read for the last time
+    const int x = rank_of(slot);
+    const bool stays = x == 2 || (x == 1 && run < want);
+    run += x == 1;
+    if (IN_SMEM) {
+      s_top[slot - s0] = stays;  // the thread's own slots, looked at for the last time
+    } else {
+      if (slot < a.keep && !stays) a.dst[list + holes_before++] = slot;
+      if (slot >= a.keep && stays) a.src[list + movers_before++] = slot;
+    }
+  }
+  if (IN_SMEM) {
+    // the lists in whole lines: the warp goes over its threads' parts, 32 slots at a time
+    __syncwarp();
+    const int lane = tid & 31;
+    uint32_t hb = __shfl_sync(0xffffffffu, holes_before, 0), mb = __shfl_sync(0xffffffffu, movers_before, 0);
+    const int first = __shfl_sync(0xffffffffu, t0, 0), last = __shfl_sync(0xffffffffu, t1, 31);
+    const uint32_t below = (1u << lane) - 1;
+    for (int base = first; base < last; base += 32) {
+      const int slot = base + lane;
+      const bool in = slot < last, stays = in && s_top[slot - s0];
+      const uint32_t h = __ballot_sync(0xffffffffu, in && !stays && slot < a.keep);
+      const uint32_t m = __ballot_sync(0xffffffffu, stays && slot >= a.keep);
+      if (h >> lane & 1) a.dst[list + hb + __popc(h & below)] = slot;
+      if (m >> lane & 1) a.src[list + mb + __popc(m & below)] = slot;
+      hb += __popc(h);
+      mb += __popc(m);
+    }
   }
   if (CLUSTER == 1) {
     __syncthreads();
