@@ -26,6 +26,8 @@
 // scheduler the exponential units idled half the time.
 // view_rows_kernel: at most four rows in all against the prefix.  Bound by the read
 // of the cache; CUDA cores, eight lanes a key, four keys' loads in flight a lane.
+// Over a short prefix latency is what counts: the blocks of a head are a cluster
+// then, whose first one takes the own keys too and joins all of it: one launch.
 // view_own_kernel: views of few rows.  Their own keys are read by CUDA cores
 // (eight lanes a key, plain 16-byte loads: nothing is read that no query sees),
 // and the partial results against the prefix are merged in the same pass.
@@ -34,6 +36,7 @@
 // Every sum, maximum and partial result is fp32; P is rounded to bf16 for the
 // product with V (a relative 2^-9 each, independent between keys), and the
 // denominator sums the unrounded weights.
+#include <cooperative_groups.h>
 #include <math.h>
 #include <math_constants.h>
 
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const ViewDims& d = a.d;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hk = blockIdx.y;
-  const int unit = blockIdx.x / a.n_split, split = blockIdx.x - unit * a.n_split;
+  const int unit = (int)(blockIdx.x / (unsigned)a.n_split), split = blockIdx.x - unit * a.n_split;
   const int MT = a.rows_tok, unit_tok = 2 * MT;
 
   // this CTA's rows [tok0, tok_end) and keys; uniform over the CTA
@@ -135,8 +138,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (d.causal) nk_seen = max(0, min(nk, last_row - q0 + nk - nq + 1));
   const int np = a.do_prefix ? (d.n_prefix + TK - 1) / TK : 0;
   const int nt_all = np + (nk_seen + TK - 1) / TK;
-  const int j0 = (int)((long long)nt_all * split / a.n_split);
-  const int nt = (int)((long long)nt_all * (split + 1) / a.n_split) - j0;
+  // at most 2^24 tiles and 64 splits
+  const int j0 = (int)((unsigned)(nt_all * split) / (unsigned)a.n_split);
+  const int nt = (int)((unsigned)(nt_all * (split + 1)) / (unsigned)a.n_split) - j0;
   // one tile of rows: issuer w and its streams take every other key tile, else
   // all key tiles of query tile w.  The i-th step is key tile j0 + at(w, i)
   const bool one = tok0 + MT >= tok_end;
@@ -598,6 +602,17 @@ struct Row {
 #pragma unroll
     for (int c = 0; c < 8; ++c) o[c] = 0.f;
   }
+  // takes a key of score s
+  __device__ __forceinline__ void add(float s, const float (&v)[8]) {
+    // exp2f(-infinity - -infinity) would be NaN for scores of -infinity
+    const float mn = fmaxf(m, s);
+    const float corr = m == mn ? 1.f : exp2f(m - mn);
+    const float p = s == -INFINITY ? 0.f : exp2f(s - mn);
+    l = l * corr + p;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = fmaf(p, v[c], o[c] * corr);
+    m = mn;
+  }
   // joins the states of the lanes that differ in bits 3 and 4
   __device__ __forceinline__ void join_groups() {
 #pragma unroll
@@ -616,18 +631,49 @@ struct Row {
 
 constexpr int ROWS_THREADS = 512, ROWS_UNROLL = 4;
 
-// Block (split, key head): rows [0, R) against the split's part of the prefix.
-template <int R>
-__global__ void __launch_bounds__(ROWS_THREADS)
-    view_rows_kernel(const ViewDims d, const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
-                     float* __restrict__ part_o, float* __restrict__ part_lse) {
-  pdl_launch();
+constexpr int ROWS_CLUSTER = 8;
+
+struct RowsArgs {
+  const bf16 *q, *kp, *vp, *ko, *vo;
+  float *part_o, *part_lse;  // JOINED false: partial results
+  bf16* out;                 // JOINED: results
+  float* lse;
+  unsigned* err;
+};
+
+// Block (split, key head): rows [0, R) against the split's part of the prefix.  With
+// JOINED the splits of a head are a cluster, and its first block finishes the rows.
+template <int R, bool JOINED>
+__global__ void __launch_bounds__(ROWS_THREADS, R == 1 && !JOINED ? 2 : 1) view_rows_kernel(const ViewDims d, const RowsArgs a) {
+  namespace cg = cooperative_groups;
+  if (JOINED)
+    cg::this_cluster().barrier_arrive();  // this block has started
+  else
+    pdl_launch();
+  const bf16* __restrict__ q = a.q;
+  const bf16* __restrict__ k = a.kp;
+  const bf16* __restrict__ v = a.vp;
   constexpr int WARPS = ROWS_THREADS / 32, GROUPS = ROWS_THREADS / 8;
-  __shared__ float s_m[WARPS][R], s_l[WARPS][R], s_o[WARPS][R][64];
+  __shared__ float s_m[WARPS][R], s_l[WARPS][R], s_o[WARPS][R][64], s_row[ROWS_CLUSTER][R][66];
   const int hk = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = (lane & 7) * 8;
   const int rows = d.n_q * d.G;
   const int j0 = (int)((long long)d.n_prefix * blockIdx.x / gridDim.x);
   const int j1 = (int)((long long)d.n_prefix * (blockIdx.x + 1) / gridDim.x);
+  const bf16* kb = k + hk * 64 + e;
+  const bf16* vb = v + hk * 64 + e;
+  uint4 ku[ROWS_UNROLL], vu[ROWS_UNROLL];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < ROWS_UNROLL; ++u) {
+      const int j = base + u * GROUPS;
+      ku[u] = vu[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (j < j1) {
+        ku[u] = *reinterpret_cast<const uint4*>(kb + j * d.kp_stride);
+        vu[u] = *reinterpret_cast<const uint4*>(vb + j * d.vp_stride);
+      }
+    }
+  };
+  if (JOINED) load(j0 + (tid >> 3));  // on their way together with the queries
   float qf[R][8];
   Row st[R];
 #pragma unroll
@@ -638,19 +684,16 @@ __global__ void __launch_bounds__(ROWS_THREADS)
     for (int c = 0; c < 8; ++c) qf[i][c] *= d.c2;
     st[i].clear();
   }
-  const bf16* kb = k + hk * 64 + e;
-  const bf16* vb = v + hk * 64 + e;
+  const bool first = JOINED && blockIdx.x == 0;
+  int q_lo = 0, q_hi = 0;
+  if (first) {
+    // looked at behind the prefix: on their way during it
+    q_lo = d.q_off[0];
+    q_hi = d.q_off[d.B];
+    asm volatile("prefetch.global.L1 [%0];\n" ::"l"(d.own_off));
+  }
   for (int base = j0 + (tid >> 3); base < j1 + (tid >> 3); base += GROUPS * ROWS_UNROLL) {
-    uint4 ku[ROWS_UNROLL], vu[ROWS_UNROLL];
-#pragma unroll
-    for (int u = 0; u < ROWS_UNROLL; ++u) {
-      const int j = base + u * GROUPS;
-      ku[u] = vu[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (j < j1) {
-        ku[u] = *reinterpret_cast<const uint4*>(kb + j * d.kp_stride);
-        vu[u] = *reinterpret_cast<const uint4*>(vb + j * d.vp_stride);
-      }
-    }
+    if (!JOINED || base >= j0 + GROUPS) load(base);
     float s[R][ROWS_UNROLL];
 #pragma unroll
     for (int u = 0; u < ROWS_UNROLL; ++u) {
@@ -692,6 +735,53 @@ __global__ void __launch_bounds__(ROWS_THREADS)
         for (int c = 0; c < 8; ++c) st[i].o[c] = fmaf(p[i][u], vf[c], st[i].o[c]);
     }
   }
+  // the first block: which own keys the rows see, and whether they belong to a view
+  int own_lo[R], own_hi[R];
+  bool mine[R];
+  if (first) {
+    if (hk == 0) {
+      ViewRange r;
+      for (int b = tid; b < d.B; b += ROWS_THREADS) view_range(d, b, &r, a.err);
+    }
+    q_lo = max(q_lo, 0);
+    q_hi = min(q_hi, d.n_q);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int tl = min(i, rows - 1) / d.G;
+      mine[i] = i < rows && tl >= q_lo && tl < q_hi;
+      own_lo[i] = own_hi[i] = 0;
+      if (!mine[i]) continue;
+      // the view of the token: the last one that starts at or before it
+      int lo = 0, hi = d.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (d.q_off[mid] <= tl) lo = mid; else hi = mid;
+      }
+      ViewRange r;
+      mine[i] = view_range(d, lo, &r, nullptr);
+      if (!mine[i]) continue;
+      const int nk = r.k1 - r.k0;
+      own_lo[i] = r.k0;
+      own_hi[i] = r.k0 + (d.causal ? max(0, min(nk, tl - r.q0 + nk - (r.q1 - r.q0) + 1)) : nk);
+    }
+  }
+  if (first) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      for (int base = own_lo[i]; base < own_hi[i]; base += GROUPS) {
+        const int j = base + (tid >> 3);
+        const bool live = j < own_hi[i];
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        float kf[8], vf[8];
+        unpack8(live ? *reinterpret_cast<const uint4*>(a.ko + j * d.ko_stride + hk * 64 + e) : zero, kf);
+        unpack8(live ? *reinterpret_cast<const uint4*>(a.vo + j * d.vo_stride + hk * 64 + e) : zero, vf);
+        float x = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x = fmaf(qf[i][c], kf[c], x);
+        x = sum8(x);
+        if (live) st[i].add(x, vf);
+      }
+  }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     st[i].join_groups();
@@ -718,9 +808,46 @@ __global__ void __launch_bounds__(ROWS_THREADS)
       o += s_o[w][i][c] * f;
     }
     const int tl = i / d.G, h = hk * d.G + i - tl * d.G;
-    const long long at = ((long long)blockIdx.x * d.n_q + tl) * d.H + h;
-    part_o[at * 64 + c] = l == 0.f ? 0.f : o / l;
-    if (c == 0) part_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
+    if (!JOINED) {
+      const long long at = ((long long)blockIdx.x * d.n_q + tl) * d.H + h;
+      a.part_o[at * 64 + c] = l == 0.f ? 0.f : o / l;
+      if (c == 0) a.part_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
+    } else {
+      // into the first block's memory
+      cg::this_cluster().barrier_wait();
+      float* to = cg::this_cluster().map_shared_rank(&s_row[blockIdx.x][i][0], 0);
+      to[c] = o;
+      if (c == 0) {
+        to[64] = m;
+        to[65] = l;
+      }
+    }
+  } else if (JOINED) {
+    cg::this_cluster().barrier_wait();
+  }
+  if (JOINED) {
+    cg::this_cluster().barrier_arrive();
+    if (!first) return;
+    cg::this_cluster().barrier_wait();
+    if (first && i < min(R, rows)) {
+      float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+      for (int r = 0; r < ROWS_CLUSTER; ++r) m = fmaxf(m, s_row[r][i][64]);
+#pragma unroll
+      for (int r = 0; r < ROWS_CLUSTER; ++r) {
+        const float mr = s_row[r][i][64], f = mr == m ? 1.f : exp2f(mr - m);
+        l += s_row[r][i][65] * f;
+        o += s_row[r][i][c] * f;
+      }
+      bool writes = false;
+#pragma unroll
+      for (int u = 0; u < R; ++u) writes = writes || (u == i && mine[u]);
+      if (writes) {
+        const int tl = i / d.G, h = hk * d.G + i - tl * d.G;
+        a.out[tl * d.o_stride + h * 64 + c] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+        if (a.lse && c == 0) a.lse[(long long)tl * d.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      }
+    }
   }
 }
 
@@ -781,16 +908,7 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
 #pragma unroll
       for (int c = 0; c < 8; ++c) s = fmaf(qf[i][c], kf[c], s);
       s = sum8(s);
-      if (j < end[i]) {
-        // exp2f(-infinity - -infinity) would be NaN for scores of -infinity
-        const float mn = fmaxf(st[i].m, s);
-        const float corr = st[i].m == mn ? 1.f : exp2f(st[i].m - mn);
-        const float p = s == -CUDART_INF_F ? 0.f : exp2f(s - mn);
-        st[i].l = st[i].l * corr + p;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) st[i].o[c] = fmaf(p, vf[c], st[i].o[c] * corr);
-        st[i].m = mn;
-      }
+      if (j < end[i]) st[i].add(s, vf);
     }
   }
   // the four groups of the warp, then the warps
@@ -853,6 +971,22 @@ cudaError_t prepare_kernel() {
   return allow_smem(view_attn_kernel, (int)kSmemBytes, &done);
 }
 
+template <int R>
+cudaError_t launch_joined(const ViewDims& d, const RowsArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ROWS_CLUSTER, (unsigned)d.Hk);
+  cfg.blockDim = dim3(ROWS_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ROWS_CLUSTER;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, view_rows_kernel<R, true>, d, a);
+}
+
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // Key splits for `units` CTAs of `tiles` key tiles each on 148 SMs.  Costs are
@@ -893,11 +1027,14 @@ ViewPlan view_plan(const ViewDims& d) {
   const double merge = 1.0 + (double)d.n_q * d.H * 64 * 8 / 3.0e6;
   p.rows = p.packed && (long long)d.n_q * d.G <= 4 && (p.small_own || !has_own);
   if (p.rows) {
-    // two blocks an SM (95 us for a token at 137400 keys of 16 heads, 117 with one);
-    // one where that would leave them few keys, for fewer results to merge
+    // one launch while its eight blocks a head keep up with the memory; two blocks an
+    // SM beyond (95 us for a token at 137400 keys of 16 heads, 117 with one)
+    p.joined = d.n_prefix <= 16384;
+    if (p.joined) {
+      p.small_own = 0;
+      return p;
+    }
     int s = 296 / d.Hk;
-    if (d.n_prefix < s * 512) s = 148 / d.Hk;
-    if (s > d.n_prefix / 128) s = d.n_prefix / 128;
     p.split_packed = s > 1 ? s : 1;
     p.parts = p.split_packed;
     return p;
@@ -926,14 +1063,17 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
   if (d.n_q <= 0) return cudaSuccess;
   const int MT = 128 / d.G;
   if (p.rows) {
-    const dim3 grid((unsigned)p.split_packed, (unsigned)d.Hk);
     const int rows = d.n_q * d.G;
+    const RowsArgs a = {q, kp, vp, ko, vo, part_o, part_lse, out, lse, err};
+    if (p.joined)
+      return rows == 1 ? launch_joined<1>(d, a, st) : rows == 2 ? launch_joined<2>(d, a, st) : launch_joined<4>(d, a, st);
+    const dim3 grid((unsigned)p.split_packed, (unsigned)d.Hk);
     if (rows == 1)
-      view_rows_kernel<1><<<grid, ROWS_THREADS, 0, st>>>(d, q, kp, vp, part_o, part_lse);
+      view_rows_kernel<1, false><<<grid, ROWS_THREADS, 0, st>>>(d, a);
     else if (rows == 2)
-      view_rows_kernel<2><<<grid, ROWS_THREADS, 0, st>>>(d, q, kp, vp, part_o, part_lse);
+      view_rows_kernel<2, false><<<grid, ROWS_THREADS, 0, st>>>(d, a);
     else
-      view_rows_kernel<4><<<grid, ROWS_THREADS, 0, st>>>(d, q, kp, vp, part_o, part_lse);
+      view_rows_kernel<4, false><<<grid, ROWS_THREADS, 0, st>>>(d, a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   } else if (p.packed || p.aligned) {

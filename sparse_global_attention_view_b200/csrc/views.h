@@ -28,6 +28,7 @@ struct ViewPlan {
   // alone, rows aligned to views against both, or against their own keys alone
   int packed, aligned, aligned_prefix, aligned_own;
   int rows;        // at most four rows: the prefix by the CUDA-core kernel, instead of `packed`
+  int joined;      // by clusters that finish the rows, own keys included
   int small_own;   // the views' own keys by the CUDA-core kernel, which also merges
   int split_packed, split_aligned;  // key splits
   int parts;       // partial results per (query, head); 0: written directly

@@ -95,11 +95,14 @@ def _rows(t, n, heads, dev, name, exact=True):
     With ``exact`` false the tensor may hold more than n tokens."""
     if n == 0:
         return None, 0
-    if isinstance(t, torch.Tensor) and t.dtype is BF16 and t.get_device() == dev and t.dim() == 3:
-        tokens, h, dim = t.shape
-        s0, s1, s2 = t.stride()
-        if (tokens == n or (not exact and tokens > n)) and h == heads and dim == 64 and s2 == 1 and (s1 == 64 or h == 1):
-            return t.data_ptr(), s0 if tokens > 1 else 0
+    if isinstance(t, torch.Tensor) and t.dtype is BF16 and t.get_device() == dev:
+        if t.shape == (n, heads, 64) and t.is_contiguous():
+            return t.data_ptr(), 0
+        if t.dim() == 3:
+            tokens, h, dim = t.shape
+            s0, s1, s2 = t.stride()
+            if (tokens == n or (not exact and tokens > n)) and h == heads and dim == 64 and s2 == 1 and (s1 == 64 or h == 1):
+                return t.data_ptr(), s0 if tokens > 1 else 0
     _refuse(t, BF16, dev, name, f"[{'' if exact else '>= '}{n}, {heads}, 64] with its heads side by side")
 
 

@@ -72,6 +72,9 @@ SIZES = {
     "one token, no prefix": (2, 2, [1], [1], 0),
     "one token, no own": (4, 2, [1], [0], 1374),
     "three rows": (3, 1, [1], [7], 1300),
+    "three rows, long": (3, 1, [1], [700], 20000),
+    "four tokens, long": (2, 2, [1, 0, 2, 1], [7, 3, 0, 130], 17000),
+    "four tokens, many own": (2, 2, [2, 1, 1], [300, 0, 1300], 100),
     "four tokens": (2, 2, [1, 2, 1], [7, 0, 130], 1300),
     "five tokens": (2, 2, [1, 3, 1], [7, 0, 130], 300),
     "no keys": (2, 2, [3, 130], [0, 0], 0),
