@@ -286,7 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(B_LF + s));
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    // no item looks at the views' own keys: their offsets are looked at here
+    if (blockIdx.x == 0 && a.own_units == 0) check_views(d, lane, 32, a.err);
+  } else {
     const int t = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t s_addr = tbase + ((uint32_t)((warp & 3) * 32) << 16) + t * 128;
     const float c2 = d.c2;
@@ -441,10 +444,7 @@ __global__ void __launch_bounds__(256)
   const bf16* k = own ? ko : kp;
   const long long stride = own ? d.ko_stride : d.kp_stride;
   const int rows = d.n_q * d.G;
-  if (blockIdx.x == 0 && hk == 0) {
-    ViewRange r;
-    for (int b = threadIdx.x; b < d.B; b += 256) view_range(d, b, &r, a.err);
-  }
+  if (blockIdx.x == 0 && hk == 0) check_views(d, threadIdx.x, 256, a.err);
   uint4 ku[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
@@ -518,10 +518,7 @@ __global__ void __launch_bounds__(OWN_THREADS)
   const ViewDims& d = a.d;
   const int hk = blockIdx.y, e = (threadIdx.x & 7) * 8;
   const int j = blockIdx.x * (OWN_THREADS / 8) + (threadIdx.x >> 3);
-  if (blockIdx.x == 0 && hk == 0) {
-    ViewRange r;
-    for (int b = threadIdx.x; b < d.B; b += OWN_THREADS) view_range(d, b, &r, a.err);
-  }
+  if (blockIdx.x == 0 && hk == 0) check_views(d, threadIdx.x, OWN_THREADS, a.err);
   const bool in = j < d.n_own && j >= d.own_off[0] && j < d.own_off[d.B];
   // the view of the key: the last one that starts at or before it
   int lo = 0, hi = d.B;
@@ -560,6 +557,8 @@ __global__ void __launch_bounds__(OWN_THREADS)
   if (in && e == 0) a.acc_out[hk * a.acc_out_stride + d.n_prefix + j] = total;
   pdl_wait();  // whoever waits for this kernel waits for the one before it too
 }
+
+__global__ void __launch_bounds__(256) check_kernel(const ViewDims d, unsigned* err) { check_views(d, threadIdx.x, 256, err); }
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
@@ -654,6 +653,11 @@ cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf
     key_weights_kernel<<<(unsigned)grid, kThreads, kSmemBytes, st>>>(mq, mkp, mko, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+  }
+  if (a.n_items == 0 && !(p.own_cores && d.n_own > 0)) {
+    // no key to weigh: offsets that say otherwise are reported
+    check_kernel<<<1, 256, 0, st>>>(d, err);
+    return cudaGetLastError();
   }
   if (p.own_cores && d.n_own > 0) {
     const dim3 grid((unsigned)ceil_div(d.n_own, OWN_THREADS / 8), (unsigned)d.Hk);

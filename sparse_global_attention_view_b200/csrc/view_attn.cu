@@ -292,10 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     // a launch that reads no own keys still reports offsets that promise some
-    if (!a.aligned && a.check_views && blockIdx.x == 0 && blockIdx.y == 0) {
-      ViewRange r;
-      for (int b = lane; b < d.B; b += 32) view_range(d, b, &r, a.err);
-    }
+    if (a.check_views && blockIdx.x == 0 && blockIdx.y == 0) check_views(d, lane, 32, a.err);
   } else if (warp >= 4) {
     // ---------------- softmax of stream x, one thread a row ----------------
     const int x = (warp - 4) >> 2, w = x >> 1, half = x & 1;
@@ -548,7 +545,8 @@ struct Merge {
 
 // Eight lanes a (token, head); every lane eight of the 64 values.
 __global__ void __launch_bounds__(256) merge_kernel(const ViewDims d, int parts, const float* part_o, const float* part_lse,
-                                                    bf16* out, float* lse) {
+                                                    bf16* out, float* lse, unsigned* err) {
+  if (blockIdx.x == 0) check_views(d, threadIdx.x, 256, err);
   const long long rh = ((long long)blockIdx.x * 256 + threadIdx.x) >> 3;
   const int e = (threadIdx.x & 7) * 8;
   const long long n = (long long)d.n_q * d.H;
@@ -739,10 +737,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, R == 1 && !JOINED ? 2 : 1) view_
   int own_lo[R], own_hi[R];
   bool mine[R];
   if (first) {
-    if (hk == 0) {
-      ViewRange r;
-      for (int b = tid; b < d.B; b += ROWS_THREADS) view_range(d, b, &r, a.err);
-    }
+    if (hk == 0) check_views(d, tid, ROWS_THREADS, a.err);
     q_lo = max(q_lo, 0);
     q_hi = min(q_hi, d.n_q);
 #pragma unroll
@@ -963,6 +958,8 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
   }
 }
 
+__global__ void __launch_bounds__(256) check_kernel(const ViewDims d, unsigned* err) { check_views(d, threadIdx.x, 256, err); }
+
 // ---------------------------------------------------------------------------
 // host
 
@@ -1061,6 +1058,11 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
                                const bf16* ko, const bf16* vo, bf16* out, float* lse, float* part_o, float* part_lse,
                                unsigned* err, cudaStream_t st) {
   if (d.n_q <= 0) return cudaSuccess;
+  if (d.max_q <= 0) {
+    // no view has a query: offsets that say otherwise are reported
+    check_kernel<<<1, 256, 0, st>>>(d, err);
+    return cudaGetLastError();
+  }
   const int MT = 128 / d.G;
   if (p.rows) {
     const int rows = d.n_q * d.G;
@@ -1105,7 +1107,7 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
       a.aligned = 0;
       a.do_prefix = 1;
       a.do_own = 0;
-      a.check_views = !p.aligned && !p.small_own;
+      a.check_views = !p.aligned && !p.small_own && !p.parts;  // the merge does it
       a.n_split = p.split_packed;
       a.units_per_view = 0;
       a.part0 = 0;
@@ -1117,6 +1119,7 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
     }
     if (p.aligned) {
       a.aligned = 1;
+      a.check_views = 0;
       a.do_prefix = p.aligned_prefix;
       a.do_own = p.aligned_own;
       a.n_split = p.split_aligned;
@@ -1138,7 +1141,7 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
   if (p.parts > 0 || (!p.packed && !p.aligned)) {
     const long long blocks = ((long long)d.n_q * d.H * 8 + 255) / 256;
     return launch_second(merge_kernel, dim3((unsigned)blocks), 256, st, d, p.parts, (const float*)part_o,
-                         (const float*)part_lse, out, lse);
+                         (const float*)part_lse, out, lse, err);
   }
   return cudaSuccess;
 }

@@ -112,5 +112,10 @@ __device__ __forceinline__ bool view_range(const ViewDims& d, int b, ViewRange* 
   }
   return true;
 }
+// Every view's, by `threads` threads.
+__device__ __forceinline__ void check_views(const ViewDims& d, int thread, int threads, unsigned* err) {
+  ViewRange r;
+  for (int b = thread; b < d.B; b += threads) view_range(d, b, &r, err);
+}
 
 }  // namespace gsa

@@ -95,7 +95,7 @@ gsa_status make_evict_dims(const gsa_cache* c, gsa::EvictDims* d, CacheLayout* l
       c->n_keep > c->n_tokens || c->w_stride < c->n_tokens || c->w_stride >= (1LL << 40))
     return GSA_ERR_INVALID_ARG;
   if (c->head_dim != gsa::kHeadDim || c->n_kv_heads > 128) return GSA_ERR_UNSUPPORTED;
-  if (c->n_tokens > INT32_MAX - 4096) return GSA_ERR_INVALID_ARG;
+  if (c->n_tokens > INT32_MAX - (1 << 20)) return GSA_ERR_INVALID_ARG;  // slots plus a stride are int32
   d->Hk = c->n_kv_heads;
   d->n = c->n_tokens;
   d->keep = c->n_keep;

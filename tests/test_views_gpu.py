@@ -523,6 +523,28 @@ def test_bad_offsets_are_reported(name):
     assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
 
 
+@pytest.mark.parametrize("H,ql,prefix", [(2, [1], 300), (2, [1], 20000), (2, [20], 300), (2, [300], 300), (2, [300], 6000),
+                                         (2, [4], 0), (2, [300], 0)])
+def test_offsets_are_looked_at_where_no_own_key_is_expected(H, ql, prefix):
+    x = make(H, H, ql, [40], prefix)
+    z = exact_lse(x)
+    none, no_queries = batch_of(x, max_own=0), batch_of(x, max_q=0)
+    for batch in (none, no_queries):
+        for call in (lambda b: attend(x, b), lambda b: weigh(x, b, z, None, 1.0)):
+            with pytest.raises(G().GsaError) as e:
+                call(batch)
+            assert e.value.status == 6
+    y = x | dict(own_off=[0, 0])
+    out, lse = attend(y, none)
+    assert_attend(y, out, lse)
+    assert_weights(y, weigh(y, none, exact_lse(y), None, 1.0), exact_lse(y), None, 1.0)
+    y = x | dict(q_off=[0, 0])
+    out, lse = attend(y, no_queries)
+    assert (out == 7).all() and (lse == 7).all()
+    w = weigh(y, no_queries, z, None, 1.0)
+    assert (w == 0).all()  # nobody looked
+
+
 def test_waits_that_run_out():
     # the hardware itself holds a waiting thread for a microsecond or so before the limit is looked at, so this takes
     # waits that are longer: the copies' on a full ring of key or query tiles
