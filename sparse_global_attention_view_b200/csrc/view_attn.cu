@@ -986,15 +986,16 @@ cudaError_t launch_joined(const ViewDims& d, const RowsArgs& a, cudaStream_t st)
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// Key splits for `units` CTAs of `tiles` key tiles each on 148 SMs.  Costs are
-// counted in key tiles: a CTA's start and end take about as long as `fixed` of
-// them, and a merged result costs `merge` more for each split.
-int choose_split(long long units, int tiles, int most, double fixed, double merge) {
+// Key splits for `units` CTAs (one with a single tile of rows counts half) of `tiles`
+// key tiles each on 148 SMs.  Costs are counted in key tiles: a CTA's start and end
+// take about as long as ten of them (measured over splits of 96 to 1152 CTAs), and a
+// merged result costs `merge` more for each split.
+int choose_split(double units, int tiles, int most, double merge) {
   int best = 1;
   double best_cost = 0;
   for (int s = 1; s <= most && s <= tiles; ++s) {
-    const double waves = (double)((units * s + 147) / 148);
-    const double cost = waves * (ceil_div(tiles, s) + fixed) + (s > 1 ? merge * s : 0.0);
+    const double waves = ceil(units * s / 148.0);
+    const double cost = waves * (ceil_div(tiles, s) + 10.0) + (s > 1 ? merge * s : 0.0);
     if (s == 1 || cost < best_cost) {
       best = s;
       best_cost = cost;
@@ -1037,16 +1038,16 @@ ViewPlan view_plan(const ViewDims& d) {
     return p;
   }
   if (p.packed) {
-    const long long units = (long long)ceil_div(d.n_q, 2 * MT) * d.Hk;
-    p.split_packed = choose_split(units, np, 64, 4.0, merge);
+    const double units = d.n_q <= 2 * MT ? 1.0 : (double)d.n_q / (2 * MT) + 0.25;
+    p.split_packed = choose_split(units * d.Hk, np, 64, merge);
     p.parts += p.split_packed;
   }
   if (p.aligned) {
-    const int unit_tok = 2 * MT;
-    long long units = (long long)d.B * ceil_div(d.max_q, unit_tok);
-    const long long bound = d.n_q / unit_tok + d.B;  // rows there are, and a ragged end a view
-    if (units > bound) units = bound;
-    p.split_aligned = choose_split(units * d.Hk, (p.aligned_prefix ? np : 0) + no, 64, 4.0, merge);
+    // rows there are, and a quarter of a CTA for the ragged end of a view
+    double units = (double)d.n_q / (2 * MT) + 0.25 * d.B;
+    const double most = (double)d.B * ceil_div(d.max_q, 2 * MT);
+    if (units > most) units = most;
+    p.split_aligned = choose_split(units * d.Hk, (p.aligned_prefix ? np : 0) + no, 64, merge);
     p.parts += p.split_aligned;
   }
   // one part that nothing else joins is the result
