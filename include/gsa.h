@@ -408,7 +408,8 @@ typedef struct {
 } gsa_view_batch;
 
 /* Bytes of workspace prefix_attn and key_weights need for `batch` (the larger of
- * the two; header included).  Host only. */
+ * the two; header included).  Host only.  Calls that share a workspace, captured
+ * ones too, must be ordered: its contents last for one call. */
 gsa_status view_workspace_size(const gsa_view_batch* batch, size_t* bytes);
 
 /*
@@ -472,7 +473,7 @@ typedef struct {
  * and behind n_keep of k and v keep what they hold, those of acc_out and ids_out
  * are not written.  acc_out and ids_out must not overlap acc and ids, so the call
  * may be repeated (it then does the same once more).
- * ws: cache_workspace_size bytes.
+ * ws: cache_workspace_size bytes, to be shared by ordered calls only.
  */
 gsa_status cache_workspace_size(const gsa_cache* cache, size_t* bytes);
 gsa_status cache_evict(const gsa_cache* cache, gsa_bf16* k, gsa_bf16* v, const float* acc, const int32_t* ids,

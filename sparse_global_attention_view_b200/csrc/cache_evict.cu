@@ -8,7 +8,7 @@
 // as sources lie behind n_keep and targets before it, moves need no order and
 // the call may be repeated.
 //
-// select_kernel: a cluster of eight CTAs a head (one for few slots), each with a
+// select_kernel: a cluster of four or eight CTAs a head (one for few slots), each with a
 // slice of the slots and the leading halves of their sort keys in shared memory
 // (16 bits tell almost all keys apart; the others, and slices that do not fit, are
 // read again).  A radix selection finds the n_keep-th key in three passes of 11,
@@ -37,6 +37,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int BINS = 2048;
 constexpr int kFewSlots = 4096;       // one CTA a head: 19 us for 2000 slots of 16 heads against 33 of a cluster and the moves'
+constexpr int kSomeSlots = 65536;      // clusters of four: 32 us for 42594 slots of 16 heads against 38 of eight; equal at 80000
 constexpr int kMaxKeys = 96 * 1024;   // sort keys of a slice in shared memory, two bytes each
 constexpr int kCopyCtas = 64;
 
@@ -123,7 +124,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int hk, int m, int
 }
 
 template <int CLUSTER, bool IN_SMEM>
-__global__ void __launch_bounds__(kThreads, CLUSTER == 1 ? 1 : 2) select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(kThreads, CLUSTER < 8 ? 1 : 2) select_kernel(const EvictArgs a) {
   extern __shared__ uint16_t s_top[];
   __shared__ Shared sh;
   const int tid = threadIdx.x;
@@ -377,8 +378,9 @@ cudaError_t launch_cache_evict(const EvictDims& d, bf16* k, bf16* v, const float
   a.k_stride = d.k_stride;
   a.v_stride = d.v_stride;
   if (d.n <= kFewSlots) return launch_select<1, true>(a, st);
-  const cudaError_t e =
-      slice_of(d.n, 8) <= kMaxKeys ? launch_select<8, true>(a, st) : launch_select<8, false>(a, st);
+  const cudaError_t e = d.n <= kSomeSlots             ? launch_select<4, true>(a, st)
+                        : slice_of(d.n, 8) <= kMaxKeys ? launch_select<8, true>(a, st)
+                                                       : launch_select<8, false>(a, st);
   if (e != cudaSuccess || a.most == 0) return e;
   const long long blocks = (long long)((a.most + MOVE_BLOCK - 1) / MOVE_BLOCK) * d.Hk;
   return launch_second(move_kernel, dim3((unsigned)blocks), MOVE_THREADS, st, a);

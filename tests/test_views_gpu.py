@@ -184,7 +184,7 @@ def evict(k, v, acc, ids, keep, recent_from, n=None):
 
 @pytest.mark.parametrize("ties", [False, True])
 @pytest.mark.parametrize("heads,n,keep", [(1, 1, 1), (2, 2, 1), (1, 31, 7), (3, 33, 32), (2, 257, 256), (16, 1705, 1374),
-                                          (2, 5000, 1), (2, 5000, 4999), (2, 5000, 5000), (4, 8191, 4096), (1, 40000, 20001), (2, 4097, 3000),
+                                          (2, 5000, 1), (2, 5000, 4999), (2, 5000, 5000), (4, 8191, 4096), (1, 40000, 20001), (2, 4097, 3000), (1, 65537, 30000),
                                           (3, 4096, 7)])
 def test_evict(heads, n, keep, ties):
     k, v, acc, ids = cache(heads, n, n + keep, ties)
