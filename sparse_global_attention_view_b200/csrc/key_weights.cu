@@ -529,9 +529,11 @@ __global__ void __launch_bounds__(OWN_THREADS)
   int tok = 0, tok_hi = 0;
   uint4 ku = make_uint4(0u, 0u, 0u, 0u);
   if (in) {
-    tok = max(d.q_off[lo], 0);
-    tok_hi = min(d.q_off[lo + 1], d.n_q);
-    if (d.causal) tok = max(tok, j - d.own_off[lo + 1] + d.q_off[lo + 1]);
+    // offsets may be anything: a row number is formed of what the buffers hold alone
+    long long see = d.q_off[lo];
+    if (d.causal) see = max(see, (long long)j - d.own_off[lo + 1] + d.q_off[lo + 1]);
+    tok = (int)min(max(see, 0ll), (long long)d.n_q);
+    tok_hi = max(min(d.q_off[lo + 1], d.n_q), 0);
     ku = *reinterpret_cast<const uint4*>(k + j * d.ko_stride + hk * 64 + e);
   }
   float total = 0.f;

@@ -523,6 +523,29 @@ def test_bad_offsets_are_reported(name):
     assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("name", list(WAYS))
+def test_offsets_may_be_any_number(name, causal):
+    # products and differences of these leave 32 bits
+    x = make(*WAYS[name])
+    batch = batch_of(x, causal)
+    z = exact_lse(x, causal)
+    good = attend(x, batch)
+    weights = weigh(x, batch, z, None, 1.0)
+    B = len(x["q_off"]) - 1
+    for wild in (-(2**31), -(2**30) - 1, 2**30, 2**30 + 2**29, 2**31 - 1):
+        for field in ("q_off", "own_off"):
+            for i in range(B + 1):
+                y = x | {field: x[field][:i] + [wild] + x[field][i + 1 :]}
+                for call in (lambda: attend(y, batch), lambda: weigh(y, batch, z, None, 1.0)):
+                    with pytest.raises(G().GsaError) as e:
+                        call()
+                    assert e.value.status == 6, (field, i, wild)
+    again = attend(x, batch)
+    assert torch.equal(again[0], good[0]) and torch.equal(again[1], good[1])
+    assert torch.equal(weigh(x, batch, z, None, 1.0), weights)
+
+
 @pytest.mark.parametrize("H,ql,prefix", [(2, [1], 300), (2, [1], 20000), (2, [20], 300), (2, [300], 300), (2, [300], 6000),
                                          (2, [4], 0), (2, [300], 0)])
 def test_offsets_are_looked_at_where_no_own_key_is_expected(H, ql, prefix):
