@@ -611,6 +611,34 @@ struct Row {
     for (int c = 0; c < 8; ++c) o[c] = fmaf(p, v[c], o[c] * corr);
     m = mn;
   }
+  // raises the maximum to scores that come; take() then turns one into its weight
+  template <int N>
+  __device__ __forceinline__ void raise(float (&s)[N]) {
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < N; ++u) mn = fmaxf(mn, s[u]);
+    const float corr = m == mn ? 1.f : exp2f(m - mn);
+    m = mn;
+    l *= corr;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] *= corr;
+  }
+  __device__ __forceinline__ void take(float s, const float (&v)[8]) {
+    const float p = s == -INFINITY ? 0.f : exp2f(s - m);
+    l += p;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = fmaf(p, v[c], o[c]);
+  }
+  // joins another state: its maximum, sum and the lane's values
+  __device__ __forceinline__ void join(float mo, float lo, const float* vo) {
+    const float mn = fmaxf(m, mo);
+    // equal maxima, two infinite ones among them, need no factor
+    const float ca = m == mn ? 1.f : exp2f(m - mn), cb = mo == mn ? 1.f : exp2f(mo - mn);
+    l = l * ca + lo * cb;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = o[c] * ca + vo[c] * cb;
+    m = mn;
+  }
   // joins the states of the lanes that differ in bits 3 and 4
   __device__ __forceinline__ void join_groups() {
 #pragma unroll
@@ -706,31 +734,14 @@ __global__ void __launch_bounds__(ROWS_THREADS, R == 1 && !JOINED ? 2 : 1) view_
         s[i][u] = base + u * GROUPS < j1 ? x : -INFINITY;
       }
     }
-    float p[R][ROWS_UNROLL];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      float mn = st[i].m;
-#pragma unroll
-      for (int u = 0; u < ROWS_UNROLL; ++u) mn = fmaxf(mn, s[i][u]);
-      const float corr = st[i].m == mn ? 1.f : exp2f(st[i].m - mn);
-      st[i].m = mn;
-      st[i].l *= corr;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) st[i].o[c] *= corr;
-#pragma unroll
-      for (int u = 0; u < ROWS_UNROLL; ++u) {
-        p[i][u] = s[i][u] == -INFINITY ? 0.f : exp2f(s[i][u] - mn);
-        st[i].l += p[i][u];
-      }
-    }
+    for (int i = 0; i < R; ++i) st[i].raise(s[i]);
 #pragma unroll
     for (int u = 0; u < ROWS_UNROLL; ++u) {
       float vf[8];
       unpack8(vu[u], vf);
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) st[i].o[c] = fmaf(p[i][u], vf[c], st[i].o[c]);
+      for (int i = 0; i < R; ++i) st[i].take(s[i][u], vf);
     }
   }
   // the first block: which own keys the rows see, and whether they belong to a view
@@ -849,37 +860,43 @@ __global__ void __launch_bounds__(ROWS_THREADS, R == 1 && !JOINED ? 2 : 1) view_
 // ---------------------------------------------------------------------------
 // own keys of views with few rows, merged with the prefix's partial results
 
-constexpr int OWN_R = 2;       // rows of a block: 87 us for 64 pose views against 93 with four
-constexpr int OWN_WARPS = 4;
 
-// One block = one view, key head and two of the view's rows.  Eight lanes hold a
-// key's 64 values; the block's 16 groups of eight take the keys in turn, each with
-// a softmax of its own, merged at the end.
-__global__ void __launch_bounds__(32 * OWN_WARPS)
+// One block = one view, key head and R of the view's rows.  Eight lanes hold a key's
+// 64 values; the block's groups of eight take the keys in turn, each with a softmax of
+// its own, merged at the end.  Bound by the latency of the key reads: a group has four
+// keys under way at a time, or two for two rows, in 64 registers so that an SM holds 32
+// warps.  256 views of a token, 250 to 500 own keys and 16 heads, prefix of 1374
+// included: 89 us at 4.5 TB/s; 126 with one key at a time, 101 with two, 110 without the
+// limit on registers.
+template <int R, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 32 / WARPS)
     view_own_kernel(const ViewDims d, const bf16* __restrict__ q, const bf16* __restrict__ k,
                     const bf16* __restrict__ v, int parts, const float* part_o, const float* part_lse, bf16* out,
                     float* lse, unsigned* err) {
+  constexpr int GROUPS = 4 * WARPS, OWN_UNROLL = R == 1 ? 4 : 2;
   const int b = blockIdx.x, hk = blockIdx.y;
   ViewRange r;
   if (!view_range(d, b, &r, err)) {
     pdl_wait();  // whoever waits for this kernel waits for the one before it too
     return;
   }
-  __shared__ float s_m[OWN_WARPS][OWN_R], s_l[OWN_WARPS][OWN_R], s_o[OWN_WARPS][OWN_R][64];
+  __shared__ float s_m[WARPS][R], s_l[WARPS][R], s_o[WARPS][R][64];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, e = (lane & 7) * 8, grp = tid >> 3;
   const int nq = r.q1 - r.q0, nk = r.k1 - r.k0, rows = nq * d.G;
   const long long n = (long long)d.n_q * d.H;
-  const int r0 = blockIdx.z * OWN_R;
+  const int r0 = blockIdx.z * R;
   if (r0 >= rows) {
     pdl_wait();
     return;
   }
-  float qf[OWN_R][8];
-  Row st[OWN_R];
-  int end[OWN_R];
+  const bf16* kb = k + (long long)r.k0 * d.ko_stride + hk * 64 + e;
+  const bf16* vb = v + (long long)r.k0 * d.vo_stride + hk * 64 + e;
+  float qf[R][8];
+  Row st[R];
+  int end[R];
   int end_max = 0;
 #pragma unroll
-  for (int i = 0; i < OWN_R; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int row = min(r0 + i, rows - 1), tl = row / d.G, h = hk * d.G + row - tl * d.G;
     unpack8(*reinterpret_cast<const uint4*>(q + (r.q0 + tl) * d.q_stride + h * 64 + e), qf[i]);
 #pragma unroll
@@ -888,27 +905,44 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
     end[i] = d.causal ? max(0, min(nk, tl + nk - nq + 1)) : nk;
     end_max = max(end_max, end[i]);
   }
-  for (int j0 = 0; j0 < end_max; j0 += 4 * OWN_WARPS) {
-    const int j = j0 + grp;
-    const bool live = j < end_max;
-    float kf[8], vf[8];
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const uint4 ku = live ? *reinterpret_cast<const uint4*>(k + (r.k0 + j) * d.ko_stride + hk * 64 + e) : zero;
-    const uint4 vu = live ? *reinterpret_cast<const uint4*>(v + (r.k0 + j) * d.vo_stride + hk * 64 + e) : zero;
-    unpack8(ku, kf);
-    unpack8(vu, vf);
+  for (int base = 0; base < end_max; base += GROUPS * OWN_UNROLL) {
+    uint4 ku[OWN_UNROLL], vu[OWN_UNROLL];
 #pragma unroll
-    for (int i = 0; i < OWN_R; ++i) {
-      float s = 0.f;
+    for (int u = 0; u < OWN_UNROLL; ++u) {
+      const int j = base + u * GROUPS + grp;
+      ku[u] = vu[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (j < end_max) {
+        ku[u] = *reinterpret_cast<const uint4*>(kb + j * d.ko_stride);
+        vu[u] = *reinterpret_cast<const uint4*>(vb + j * d.vo_stride);
+      }
+    }
+    float s[R][OWN_UNROLL];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) s = fmaf(qf[i][c], kf[c], s);
-      s = sum8(s);
-      if (j < end[i]) st[i].add(s, vf);
+    for (int u = 0; u < OWN_UNROLL; ++u) {
+      float kf[8];
+      unpack8(ku[u], kf);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        float x = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x = fmaf(qf[i][c], kf[c], x);
+        x = sum8(x);
+        s[i][u] = base + u * GROUPS + grp < end[i] ? x : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) st[i].raise(s[i]);
+#pragma unroll
+    for (int u = 0; u < OWN_UNROLL; ++u) {
+      float vf[8];
+      unpack8(vu[u], vf);
+#pragma unroll
+      for (int i = 0; i < R; ++i) st[i].take(s[i][u], vf);
     }
   }
-  // the four groups of the warp, then the warps
+  // the four groups of a warp, then the warps
 #pragma unroll
-  for (int i = 0; i < OWN_R; ++i) {
+  for (int i = 0; i < R; ++i) {
     st[i].join_groups();
     if (lane < 8) {
 #pragma unroll
@@ -921,17 +955,15 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
   }
   __syncthreads();
   if (parts > 0) pdl_wait();
-  // warp i: row i.  Its four groups take the own results of a warp each, and the
-  // prefix's in turn
-  if (warp >= OWN_R || r0 + warp >= rows) return;
+  // warp i: row i.  Its four groups take the warps' own results in turn, and then the
+  // prefix's
+  if (warp >= R || r0 + warp >= rows) return;
   Row x;
   x.clear();
   const int row = r0 + warp, tl = row / d.G, h = hk * d.G + row - tl * d.G, tok = r.q0 + tl;
   const long long rh = (long long)tok * d.H + h;
-  x.m = s_m[lane >> 3][warp];
-  x.l = s_l[lane >> 3][warp];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) x.o[c] = s_o[lane >> 3][warp][e + c];
+  for (int w = lane >> 3; w < WARPS; w += 4) x.join(s_m[w][warp], s_l[w][warp], &s_o[w][warp][e]);
 #pragma unroll 2
   for (int p = lane >> 3; p < parts; p += 4) {
     const float z = part_lse[p * n + rh];
@@ -939,12 +971,7 @@ __global__ void __launch_bounds__(32 * OWN_WARPS)
     const float4 y0 = src[0], y1 = src[1];
     if (z == -INFINITY) continue;  // nothing was written
     const float pv[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-    const float mn = fmaxf(x.m, z);
-    const float ca = x.m == mn ? 1.f : exp2f(x.m - mn), cb = z == mn ? 1.f : exp2f(z - mn);
-    x.l = x.l * ca + cb;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) x.o[c] = x.o[c] * ca + pv[c] * cb;
-    x.m = mn;
+    x.join(z, 1.f, pv);
   }
   x.join_groups();
   if (lane < 8) {
@@ -1132,11 +1159,20 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
     }
   }
   if (p.small_own) {
-    const dim3 grid((unsigned)d.B, (unsigned)d.Hk, (unsigned)ceil_div((long long)d.max_q * d.G, OWN_R));
+    // two rows a block share the reads (64 us for 64 views of four tokens and 250 to 500
+    // own keys, 77 with one), or one where views have no more; large blocks where there are
+    // few of them and many keys (69 us for 16 tokens with up to 4000 own keys, 226 with
+    // small ones and one key at a time)
+    const int rows = d.max_q * d.G, r = rows > 1 ? 2 : 1;
+    const bool large = d.max_own >= 256 && (long long)d.B * d.Hk * ceil_div(rows, r) < 8 * 148;
+    const dim3 grid((unsigned)d.B, (unsigned)d.Hk, (unsigned)ceil_div(rows, r));
+    auto kernel = r == 1 ? (large ? view_own_kernel<1, 16> : view_own_kernel<1, 4>)
+                         : (large ? view_own_kernel<2, 16> : view_own_kernel<2, 4>);
+    const unsigned threads = large ? 512 : 128;
     if (p.parts > 0)
-      return launch_second(view_own_kernel, grid, 32 * OWN_WARPS, st, d, q, ko, vo, p.parts, (const float*)part_o,
-                           (const float*)part_lse, out, lse, err);
-    view_own_kernel<<<grid, 32 * OWN_WARPS, 0, st>>>(d, q, ko, vo, 0, part_o, part_lse, out, lse, err);
+      return launch_second(kernel, grid, threads, st, d, q, ko, vo, p.parts, (const float*)part_o, (const float*)part_lse, out,
+                           lse, err);
+    kernel<<<grid, threads, 0, st>>>(d, q, ko, vo, 0, part_o, part_lse, out, lse, err);
     return cudaGetLastError();
   }
   if (p.parts > 0 || (!p.packed && !p.aligned)) {

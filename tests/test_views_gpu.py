@@ -524,6 +524,20 @@ def test_bad_offsets_are_reported(name):
 
 
 @pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("H,Hk,ql,tl,prefix", [
+    (2, 2, [1] * 9, [4000, 0, 1, 255, 256, 257, 31, 4096, 2], 700),   # blocks of 16 warps, one row
+    (2, 2, [3, 1, 4, 2, 0, 3], [4000, 3, 4096, 0, 300, 65], 0),       # two rows, an odd number of them
+    (4, 1, [1, 4, 3, 2], [2000, 511, 513, 4096], 300),                # rows of a key head's group
+    (5, 1, [3, 2, 1], [1030, 17, 700], 300),
+    (64, 64, [1] * 40, [300 - i for i in range(40)], 130),            # blocks of four warps
+    (32, 32, [2] * 40, [300 + 7 * i for i in range(40)], 130),
+    (2, 2, [1] * 70, [i % 3 for i in range(70)], 300),                # keys of several views and of none, side by side
+])
+def test_few_rows_over_many_own_keys(H, Hk, ql, tl, prefix, causal):
+    everything(make(H, Hk, ql, tl, prefix), causal)
+
+
+@pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("name", list(WAYS))
 def test_offsets_may_be_any_number(name, causal):
     # products and differences of these leave 32 bits
