@@ -11,15 +11,15 @@
 // select_kernel: a cluster of four or eight CTAs a head (one for few slots), each with a
 // slice of the slots and the leading halves of their sort keys in shared memory
 // (16 bits tell almost all keys apart; the others, and slices that do not fit, are
-// read again).  A radix selection finds the n_keep-th key in three passes of 11,
-// 11 and 10 bits: the CTAs add their counts of each digit to one another's shared
-// memory, one barrier a pass.  Then the counts of equal keys, of free slots and of
-// movers before every thread's part of the slots give each its rank.  Integer
-// arithmetic throughout, so the result depends on the inputs alone.  Bound by
-// instruction issue and latency, not by its bytes: counting takes the slots thread
-// by thread with a run of equal digits held in a register (a cache of equal
-// accounts would queue up at one counter), ranking gives every thread an odd
-// number of consecutive slots (no votes, one scan of the block).  CTAs behind the
+// read again).  A radix selection finds the n_keep-th key in four passes of 11, 5, 8
+// and 8 bits, the first two on the halves in shared memory: every CTA adds up all
+// CTAs' counts of a digit, one barrier a pass.  Then every warp counts the kept and
+// the equal keys of its consecutive slots by votes, one scan gives what lies before
+// them, and a second round of votes the ranks.  Integer arithmetic throughout, so
+// the result depends on the inputs alone.  Bound by instruction issue and latency,
+// not by its bytes: the first digits are counted as the keys arrive, with a run of
+// equal ones held in a register (a cache of equal accounts would queue up at one
+// counter), and the second ones at a counter a lane.  CTAs behind the
 // clusters' copy the accounts and numbers of all slots below n_keep meanwhile;
 // the movers' come over those of the free slots afterwards.  The single CTA of few
 // slots does all of it, the moves as well: one launch.
@@ -35,17 +35,29 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int BINS = 2048;
 constexpr int kFewSlots = 4096;       // one CTA a head: 19 us for 2000 slots of 16 heads against 33 of a cluster and the moves'
 constexpr int kSomeSlots = 65536;      // clusters of four: 32 us for 42594 slots of 16 heads against 38 of eight; equal at 80000
 constexpr int kMaxKeys = 96 * 1024;   // sort keys of a slice in shared memory, two bytes each
 constexpr int kCopyCtas = 64;
 
+// Passes of the radix selection: a digit's place, its bins and their place among the counts.
+constexpr int kPasses = 4;
+struct Pass {
+  int shift, bins, at;
+};
+__device__ constexpr Pass kPass[kPasses] = {{21, 2048, 0}, {16, 32, 2048}, {8, 256, 2080}, {0, 256, 2336}};
+constexpr int kCounts = 2592;
+constexpr int kClose = 1024;  // slots whose half equals the limit's that a CTA remembers
+
 struct Shared {
-  uint32_t counts[BINS];   // this CTA's
-  uint32_t sums[2][BINS];  // the cluster's, one pass in use while the other is cleared
+  alignas(16) uint32_t counts[kCounts];  // this CTA's, read by the others
+  uint32_t lanes[32 * 32];  // of the second pass, for each lane of a warp
+  int close_slot[kClose];
+  uint16_t close_low[kClose];  // the lower halves of their keys
+  uint32_t n_close;
   uint32_t warp_sum[kWarps];
-  uint32_t tot[4];         // this CTA's counts, read by the others
+  uint32_t warp_tot[4][kWarps];
+  alignas(16) uint32_t tot[4];  // this CTA's counts, read by the others
   uint32_t bin, above;     // the bin that holds the wanted key; keys above it
 };
 
@@ -153,67 +165,89 @@ __global__ void __launch_bounds__(kThreads, CLUSTER < 8 ? 1 : 2) select_kernel(c
   const int rank = CLUSTER > 1 ? (int)cluster.block_rank() : 0, hk = blockIdx.x / CLUSTER;
   const float* acc = a.acc + hk * a.w_stride;
   const int* ids = a.ids + hk * a.w_stride;
-  // this CTA's slots [s0, s1), and the thread's part [t0, t1) of them
+  // this CTA's slots [s0, s1), and the warp's part [first, last) of them
+  const int lane = tid & 31, warp = tid >> 5;
   const int slice = ((a.n + CLUSTER - 1) / CLUSTER + 31) & ~31;
   const int s0 = min(a.n, rank * slice), s1 = min(a.n, s0 + slice);
-  const int part = ((s1 - s0 + kThreads - 1) / kThreads) | 1;
-  const int t0 = min(s1, s0 + tid * part), t1 = min(s1, t0 + part);
+  const int part = ((s1 - s0 + kThreads - 1) / kThreads) * 32;
+  const int first = min(s1, s0 + warp * part), last = min(s1, first + part);
   auto key_of = [&](int slot) -> uint32_t { return sort_key(acc[slot], ids[slot], a.recent_from); };
   auto top_of = [&](int slot) -> uint32_t { return IN_SMEM ? s_top[slot - s0] : key_of(slot) >> 16; };
-  if (IN_SMEM) {
-#pragma unroll 8
-    for (int s = s0 + tid; s < s1; s += kThreads) s_top[s - s0] = (uint16_t)(key_of(s) >> 16);
-  }
-  for (int b = tid; b < BINS; b += kThreads) {
-    sh.counts[b] = 0;
-    sh.sums[0][b] = 0;
-  }
-  sync_all();
+  for (int b = tid; b < kCounts; b += kThreads) sh.counts[b] = 0;
+  sh.lanes[tid] = 0;
+  if (tid == 0) sh.n_close = 0;
+  __syncthreads();
 
   // the n_keep-th largest key: its leading bits are settled pass by pass
-  uint32_t prefix = 0, mask = 0, want = (uint32_t)a.keep;
-  const int shifts[3] = {21, 10, 0};
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = shifts[pass];
-    const uint32_t bins = pass == 2 ? 1024u : 2048u;
-    uint32_t run_bin = 0, run = 0;  // equal digits seen in a row
-    auto flush = [&]() {
-      if (run) atomicAdd(&sh.counts[run_bin], run);
-    };
-#pragma unroll 4
-    for (int slot = s0 + tid; slot < s1; slot += kThreads) {
-      uint32_t k = top_of(slot) << 16;
-      if ((k ^ prefix) & mask & 0xffff0000u) continue;
-      if (pass > 0) {
-        k = key_of(slot);
-        if ((k ^ prefix) & mask) continue;
-      }
-      const uint32_t bin = (k >> shift) & (bins - 1);
-      if (bin != run_bin) {
-        flush();
-        run = 0;
-        run_bin = bin;
-      }
-      ++run;
-    }
-    flush();
-    __syncthreads();
-    // to every CTA's sums; the counts and the other sums are cleared for the next pass
-    uint32_t* sums = sh.sums[pass & 1];
-    for (int b = tid; b < BINS; b += kThreads) {
-      const uint32_t c = sh.counts[b];
-      sh.counts[b] = 0;
-      sh.sums[(pass & 1) ^ 1][b] = 0;
-      if (c) {
+  uint32_t prefix = 0, want = (uint32_t)a.keep;
 #pragma unroll
-        for (int r = 0; r < CLUSTER; ++r) atomicAdd(of_rank(sums, r) + b, c);
+  for (int pass = 0; pass < kPasses; ++pass) {
+    uint32_t* counts = sh.counts + kPass[pass].at;
+    const int shift = kPass[pass].shift;
+    const uint32_t bins = kPass[pass].bins;
+    if (pass == 0) {
+      uint32_t run_bin = 0, run = 0;  // equal digits seen in a row
+      auto flush = [&]() {
+        if (run) atomicAdd(&counts[run_bin], run);
+      };
+      for (int slot = first + lane; slot < last; slot += 128) {
+        uint32_t k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) k[u] = slot + 32 * u < last ? key_of(slot + 32 * u) : 0u;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (slot + 32 * u >= last) break;
+          if (IN_SMEM) s_top[slot + 32 * u - s0] = (uint16_t)(k[u] >> 16);
+          const uint32_t bin = k[u] >> shift;
+          if (bin != run_bin) {
+            flush();
+            run = 0;
+            run_bin = bin;
+          }
+          ++run;
+        }
+      }
+      flush();
+    } else if (pass == 1) {
+#pragma unroll 4
+      for (int slot = first + lane; slot < last; slot += 32) {
+        const uint32_t t = top_of(slot);
+        if (t >> 5 == prefix >> 21) atomicAdd(&sh.lanes[(t & 31) * 32 + lane], 1u);
+      }
+      __syncthreads();
+      const uint32_t c = __reduce_add_sync(0xffffffffu, sh.lanes[tid]);
+      if (lane == 0) counts[warp] = c;
+    } else if (pass == 3 && sh.n_close <= kClose) {
+      if (tid < sh.n_close && sh.close_low[tid] >> 8 == (prefix >> 8 & 0xff)) atomicAdd(&counts[sh.close_low[tid] & 0xff], 1u);
+    } else {
+#pragma unroll 4
+      for (int slot = first + lane; slot < last; slot += 32) {
+        if (top_of(slot) != prefix >> 16) continue;
+        const uint32_t k = key_of(slot);
+        if (pass == 2) {
+          const uint32_t at = atomicAdd(&sh.n_close, 1u);
+          if (at < kClose) {
+            sh.close_slot[at] = slot;
+            sh.close_low[at] = (uint16_t)k;
+          }
+        } else if (k >> 8 != prefix >> 8) {
+          continue;
+        }
+        atomicAdd(&counts[(k >> shift) & (bins - 1)], 1u);
       }
     }
     sync_all();
     // two bins a thread from the top: the one in which the count reaches `want`
     const int hi = (int)bins - 1 - 2 * tid;
-    const uint32_t c0 = hi > 0 ? sums[hi] : 0, c1 = hi > 0 ? sums[hi - 1] : 0;
-    uint32_t total;
+    uint32_t c0 = 0, c1 = 0, total;
+    if (hi > 0) {
+#pragma unroll
+      for (int r = 0; r < CLUSTER; ++r) {
+        const uint2 c = *reinterpret_cast<const uint2*>(of_rank(counts, r) + hi - 1);
+        c0 += c.y;
+        c1 += c.x;
+      }
+    }
     const uint32_t above = threads_before(c0 + c1, sh.warp_sum, &total);
     if (above < want && above + c0 >= want) {
       sh.bin = hi;
@@ -225,93 +259,112 @@ __global__ void __launch_bounds__(kThreads, CLUSTER < 8 ? 1 : 2) select_kernel(c
     __syncthreads();
     want -= sh.above;
     prefix |= sh.bin << shift;
-    mask |= (bins - 1) << shift;
   }
   const uint32_t limit = prefix;  // `want` of the keys that equal it stay
 
+  // Halves that equal the limit's are told apart in shared memory, so that they are
+  // enough from here on: no key's half is 0 or 0xffff.
   const uint32_t limit_top = limit >> 16;
-  // above the limit (2), equal to it (1) or below
-  auto rank_of = [&](int slot) -> int {
-    const uint32_t t = top_of(slot);
-    if (t != limit_top) return t > limit_top ? 2 : 0;
-    const uint32_t k = key_of(slot);
-    return k > limit ? 2 : (k == limit ? 1 : 0);
-  };
-  // kept for certain, and equal to the limit, before and behind `keep`
-  uint32_t more_low = 0, more_high = 0, eq_low = 0, eq_high = 0, total;
-  for (int slot = t0; slot < t1; ++slot) {
-    const int x = rank_of(slot);
-    const bool low = slot < a.keep;
-    more_low += low && x == 2;
-    more_high += !low && x == 2;
-    eq_low += low && x == 1;
-    eq_high += !low && x == 1;
+  if (IN_SMEM) {
+    auto tell = [&](int slot, uint32_t low) {
+      if (low != (limit & 0xffff)) s_top[slot - s0] = (uint16_t)(low > (limit & 0xffff) ? limit_top + 1 : limit_top - 1);
+    };
+    if (sh.n_close <= kClose) {
+      if (tid < sh.n_close) tell(sh.close_slot[tid], sh.close_low[tid]);
+    } else {
+#pragma unroll 4
+      for (int slot = first + lane; slot < last; slot += 32)
+        if (s_top[slot - s0] == limit_top) tell(slot, key_of(slot) & 0xffff);
+    }
+    __syncthreads();
   }
-  // equal keys before the thread's part: in the CTA, then in the cluster
-  uint32_t eq_before = threads_before(eq_low + eq_high, sh.warp_sum, &total);
-  if (tid == 0) sh.tot[0] = total;
+  auto short_key = [&](int slot) -> uint32_t { return IN_SMEM ? s_top[slot - s0] : key_of(slot); };
+  const uint32_t z = IN_SMEM ? limit_top : limit;
+  // kept for certain, and equal to the limit, before `keep` and from there on
+  const int low_last = min(last, a.keep), high_first = max(first, a.keep);
+  uint32_t tot[4] = {0u, 0u, 0u, 0u};
+  auto count = [&](int from, int to, uint32_t* more, uint32_t* equal) {
+#pragma unroll 4
+    for (int slot = from + lane; slot < to; slot += 32) {
+      const uint32_t k = short_key(slot);
+      *more += k > z;
+      *equal += k == z;
+    }
+  };
+  count(first, low_last, &tot[0], &tot[1]);
+  count(high_first, last, &tot[2], &tot[3]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tot[c] = __reduce_add_sync(0xffffffffu, tot[c]);
+  // ... before the warp's part: in the CTA, then in the cluster
+  if (lane == 0)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sh.warp_tot[c][warp] = tot[c];
+  __syncthreads();
+  uint32_t before[4], all[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t x = sh.warp_tot[c][lane];
+    before[c] = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0u);
+    const uint32_t sum = __reduce_add_sync(0xffffffffu, x);
+    if (tid == 0) sh.tot[c] = sum;
+  }
   sync_all();
-  for (int r = 0; r < rank; ++r) eq_before += of_rank(sh.tot, r)[0];
-  // free slots below `keep`, and kept tokens at or behind it
-  const uint32_t left = want > eq_before ? want - eq_before : 0;
-  const uint32_t stay_low = min(left, eq_low), stay_high = min(left - stay_low, eq_high);
-  const uint32_t holes = (uint32_t)max(0, min(t1, a.keep) - t0) - more_low - stay_low, movers = more_high + stay_high;
-  uint32_t holes_before = threads_before(holes, sh.warp_sum, &total);
-  if (tid == 0) sh.tot[1] = total;
-  uint32_t movers_before = threads_before(movers, sh.warp_sum, &total);
-  if (tid == 0) sh.tot[2] = total;
-  sync_all();
-  uint32_t all = 0;
 #pragma unroll
   for (int r = 0; r < CLUSTER; ++r) {
-    const uint32_t* t = of_rank(sh.tot, r);
-    if (r < rank) {
-      holes_before += t[1];
-      movers_before += t[2];
-    }
-    all += t[2];
-  }
-  if (rank == 0 && tid == 0) a.n_moves[hk] = (int)all;
-  const long long list = (long long)hk * a.most;
-  uint32_t run = eq_before;
-  for (int slot = t0; slot < t1; ++slot) {
-    const int x = rank_of(slot);
-    const bool stays = x == 2 || (x == 1 && run < want);
-    run += x == 1;
-    if (IN_SMEM) {
-      s_top[slot - s0] = stays;  // the thread's own slots, looked at for the last time
-    } else {
-      if (slot < a.keep && !stays) a.dst[list + holes_before++] = slot;
-      if (slot >= a.keep && stays) a.src[list + movers_before++] = slot;
+    const uint4 t = *reinterpret_cast<const uint4*>(of_rank(sh.tot, r));
+    const uint32_t tc[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (r < rank) before[c] += tc[c];
+      all[c] += tc[c];
     }
   }
-  if (IN_SMEM) {
-    // the lists in whole lines: the warp goes over its threads' parts, 32 slots at a time
-    __syncwarp();
-    const int lane = tid & 31;
-    uint32_t hb = __shfl_sync(0xffffffffu, holes_before, 0), mb = __shfl_sync(0xffffffffu, movers_before, 0);
-    const int first = __shfl_sync(0xffffffffu, t0, 0), last = __shfl_sync(0xffffffffu, t1, 31);
-    const uint32_t below = (1u << lane) - 1;
-    for (int base = first; base < last; base += 32) {
-      const int slot = base + lane;
-      const bool in = slot < last, stays = in && s_top[slot - s0];
-      const uint32_t h = __ballot_sync(0xffffffffu, in && !stays && slot < a.keep);
-      const uint32_t m = __ballot_sync(0xffffffffu, stays && slot >= a.keep);
-      if (h >> lane & 1) a.dst[list + hb + __popc(h & below)] = slot;
-      if (m >> lane & 1) a.src[list + mb + __popc(m & below)] = slot;
-      hb += __popc(h);
-      mb += __popc(m);
+  // the equal keys that stay are the first ones, so those below `keep` before others
+  auto stay_low = [&](const uint32_t (&t)[4]) -> uint32_t { return min(want, t[1]); };
+  auto stay_high = [&](const uint32_t (&t)[4]) -> uint32_t { return min(want - stay_low(t), t[3]); };
+  const uint32_t n_moves = all[2] + stay_high(all);
+  if (rank == 0 && tid == 0) a.n_moves[hk] = (int)n_moves;
+  // free slots below `keep`, and kept tokens at or behind it, before the warp's own
+  uint32_t holes = (uint32_t)min(first, a.keep) - before[0] - stay_low(before);
+  uint32_t movers = before[2] + stay_high(before), run = before[1] + before[3];
+  const long long row = hk * a.w_stride;
+  int* const dst = a.dst + (long long)hk * a.most;
+  int* const src = a.src + (long long)hk * a.most;
+  const uint32_t below = (1u << lane) - 1;
+  const bool ties = all[1] + all[3] > want;  // not all equal keys stay
+  auto stays = [&](int slot, int to) -> bool {
+    const uint32_t k = slot < to ? short_key(slot) : 0u;
+    bool yes = k >= z;
+    if (ties) {
+      const uint32_t q = __ballot_sync(0xffffffffu, k == z);
+      if (k == z) yes = run + __popc(q & below) < want;
+      run += __popc(q);
     }
+    return yes;
+  };
+#pragma unroll 2
+  for (int base = first; base < low_last; base += 32) {
+    const int slot = base + lane;
+    const bool yes = stays(slot, low_last), hole = !yes && slot < low_last;
+    const uint32_t h = __ballot_sync(0xffffffffu, hole);
+    if (hole) dst[holes + __popc(h & below)] = slot;
+    holes += __popc(h);
+    if (CLUSTER == 1 && yes) {
+      a.acc_out[row + slot] = acc[slot];
+      a.ids_out[row + slot] = ids[slot];
+    }
+  }
+#pragma unroll 2
+  for (int base = high_first; base < last; base += 32) {
+    const int slot = base + lane;
+    const bool yes = stays(slot, last);
+    const uint32_t m = __ballot_sync(0xffffffffu, yes);
+    if (yes) src[movers + __popc(m & below)] = slot;
+    movers += __popc(m);
   }
   if (CLUSTER == 1) {
     __syncthreads();
-    const long long row = hk * a.w_stride;
-    for (int slot = tid; slot < a.keep; slot += kThreads)
-      if (s_top[slot]) {
-        a.acc_out[row + slot] = acc[slot];
-        a.ids_out[row + slot] = ids[slot];
-      }
-    for (int m = tid >> 3; m < (int)all; m += kThreads / 8 * MOVE_UNROLL) move_rows(a, hk, m, kThreads / 8, (int)all);
+    for (int m = tid >> 3; m < (int)n_moves; m += kThreads / 8 * MOVE_UNROLL) move_rows(a, hk, m, kThreads / 8, (int)n_moves);
   }
   sync_all();  // no CTA leaves while another may read its shared memory
 }
