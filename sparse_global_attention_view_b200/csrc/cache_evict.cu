@@ -35,9 +35,12 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kFewSlots = 4096;       // one CTA a head: 19 us for 2000 slots of 16 heads against 33 of a cluster and the moves'
-constexpr int kSomeSlots = 65536;      // clusters of four: 32 us for 42594 slots of 16 heads against 38 of eight; equal at 80000
-constexpr int kMaxKeys = 96 * 1024;   // sort keys of a slice in shared memory, two bytes each
+constexpr int kFewSlots = 4096;       // one CTA a head: 14 us for 2500 slots of 16 heads against 18 of a cluster and the moves'
+constexpr int kSomeSlots = 65536;      // clusters of four: 22 us for 20000 slots of 16 heads against 31 of eight; equal at 80000
+// Halves of sort keys in a slice's shared memory, so that two CTAs fit on an SM: 162 us
+// for 274800 slots of 16 heads against 185 without; with 400000 slots and one CTA on an
+// SM, 303 against 254 without.
+constexpr int kMaxKeys = 44 * 1024;
 constexpr int kCopyCtas = 64;
 
 // Passes of the radix selection: a digit's place, its bins and their place among the counts.
