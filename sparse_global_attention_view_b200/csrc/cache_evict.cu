@@ -111,15 +111,15 @@ __device__ __forceinline__ uint32_t threads_before(uint32_t v, uint32_t* scratch
   return __shfl_sync(0xffffffffu, w - own, warp) + sum - v;
 }
 
-// Moves m, m + step, ... of a head (MOVE_UNROLL of them); eight lanes a move.
-constexpr int MOVE_UNROLL = 2;
+// Moves m, m + step, ... of a head (N of them); eight lanes a move.
+template <int N>
 __device__ __forceinline__ void move_rows(const EvictArgs& a, int hk, int m, int step, int n) {
   const int e = (threadIdx.x & 7) * 8;
   const long long list = (long long)hk * a.most, row = hk * a.w_stride;
-  uint4 kk[MOVE_UNROLL], vv[MOVE_UNROLL];
-  int to[MOVE_UNROLL];
+  uint4 kk[N], vv[N];
+  int to[N];
 #pragma unroll
-  for (int u = 0; u < MOVE_UNROLL; ++u, m += step) {
+  for (int u = 0; u < N; ++u, m += step) {
     to[u] = -1;
     if (m < n) {
       const int from = a.src[list + m];
@@ -131,7 +131,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int hk, int m, int
     }
   }
 #pragma unroll
-  for (int u = 0; u < MOVE_UNROLL; ++u)
+  for (int u = 0; u < N; ++u)
     if (to[u] >= 0) {
       *reinterpret_cast<uint4*>(a.k + to[u] * a.k_stride + hk * 64 + e) = kk[u];
       *reinterpret_cast<uint4*>(a.v + to[u] * a.v_stride + hk * 64 + e) = vv[u];
@@ -367,20 +367,20 @@ __global__ void __launch_bounds__(kThreads, CLUSTER < 8 ? 1 : 2) select_kernel(c
   }
   if (CLUSTER == 1) {
     __syncthreads();
-    for (int m = tid >> 3; m < (int)n_moves; m += kThreads / 8 * MOVE_UNROLL) move_rows(a, hk, m, kThreads / 8, (int)n_moves);
+    for (int m = tid >> 3; m < (int)n_moves; m += kThreads / 8 * 2) move_rows<2>(a, hk, m, kThreads / 8, (int)n_moves);
   }
   sync_all();  // no CTA leaves while another may read its shared memory
 }
 
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_BLOCK = MOVE_THREADS / 8 * MOVE_UNROLL;  // moves of a block
 
+template <int N>
 __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const EvictArgs a) {
   // heads vary fastest: equal ranks of all heads lie near one another in memory
-  const int hk = blockIdx.x % a.Hk, m0 = blockIdx.x / a.Hk * MOVE_BLOCK;
+  const int hk = blockIdx.x % a.Hk, m0 = blockIdx.x / a.Hk * (MOVE_THREADS / 8 * N);
   pdl_wait();
   const int n = a.n_moves[hk];
-  if (m0 < n) move_rows(a, hk, m0 + (threadIdx.x >> 3), MOVE_THREADS / 8, n);
+  if (m0 < n) move_rows<N>(a, hk, m0 + (threadIdx.x >> 3), MOVE_THREADS / 8, n);
 }
 
 int slice_of(int n, int cluster) { return ((n + cluster - 1) / cluster + 31) & ~31; }
@@ -438,8 +438,13 @@ cudaError_t launch_cache_evict(const EvictDims& d, bf16* k, bf16* v, const float
                         : slice_of(d.n, 8) <= kMaxKeys ? launch_select<8, true>(a, st)
                                                        : launch_select<8, false>(a, st);
   if (e != cudaSuccess || a.most == 0) return e;
-  const long long blocks = (long long)((a.most + MOVE_BLOCK - 1) / MOVE_BLOCK) * d.Hk;
-  return launch_second(move_kernel, dim3((unsigned)blocks), MOVE_THREADS, st, a);
+  // two moves a thread at a time (162 us for 274800 -> 137400 slots of 16 heads; 178 with
+  // one, 176 with four), one while that makes two waves of blocks at most (20.6 us for
+  // 42594 -> 41220, 22.6 with two; equal at 24000 -> 18000)
+  auto blocks = [&](int per) -> long long { return (long long)((a.most + per - 1) / per) * d.Hk; };
+  constexpr int kRows = MOVE_THREADS / 8;
+  if (blocks(kRows) <= 16 * 148) return launch_second(move_kernel<1>, dim3((unsigned)blocks(kRows)), MOVE_THREADS, st, a);
+  return launch_second(move_kernel<2>, dim3((unsigned)blocks(2 * kRows)), MOVE_THREADS, st, a);
 }
 
 }  // namespace gsa
