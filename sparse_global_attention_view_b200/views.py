@@ -92,7 +92,8 @@ def _refuse(t, dtype, dev, name, want):
 def _rows(t, n, heads, dev, name, exact=True):
     """Pointer and token stride of bf16 [n][heads][64] whose heads lie side by side; (None, 0) when n is 0.
 
-    With ``exact`` false the tensor may hold more than n tokens."""
+    With ``exact`` false the tensor may hold more than n tokens.  Tokens that share memory (an expanded tensor's,
+    whose stride is 0) are refused: the C ABI's stride 0 is a dense layout."""
     if n == 0:
         return None, 0
     if isinstance(t, torch.Tensor) and t.dtype is BF16 and t.get_device() == dev:
@@ -101,7 +102,8 @@ def _rows(t, n, heads, dev, name, exact=True):
         if t.dim() == 3:
             tokens, h, dim = t.shape
             s0, s1, s2 = t.stride()
-            if (tokens == n or (not exact and tokens > n)) and h == heads and dim == 64 and s2 == 1 and (s1 == 64 or h == 1):
+            if ((tokens == n or (not exact and tokens > n)) and h == heads and dim == 64 and s2 == 1 and (s1 == 64 or h == 1)
+                    and (s0 >= 64 * h or tokens == 1)):
                 return t.data_ptr(), s0 if tokens > 1 else 0
     _refuse(t, BF16, dev, name, f"[{'' if exact else '>= '}{n}, {heads}, 64] with its heads side by side")
 

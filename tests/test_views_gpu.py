@@ -626,6 +626,26 @@ def test_python_refusals():
         G().cache_evict(101, 50, 100, k, v, acc, ids, torch.empty_like(acc), torch.empty_like(ids), evict_ws)
 
 
+def test_expanded_tensors_are_refused():
+    x = make(2, 2, [5], [5], 300)
+    batch = batch_of(x)
+    ws, off = G().new_view_workspace(batch), ints([0, 5])
+    out, lse = torch.empty_like(x["q"]), torch.empty(5, 2, device=DEV)
+    args = [x["q"], x["kp"], x["vp"], x["ko"], x["vo"], off, off, out, lse, ws]
+    shared = lambda t: t[:1].expand_as(t)  # noqa: E731
+    for i in (0, 1, 2, 3, 4, 7):
+        with pytest.raises(ValueError):
+            G().prefix_attn(batch, *args[:i], shared(args[i]), *args[i + 1:])
+    args = [x["q"], x["kp"], x["ko"], off, off, lse, None, torch.empty(2, 305, device=DEV), 1.0, ws]
+    for i in (0, 1, 2):
+        with pytest.raises(ValueError):
+            G().key_weights(batch, *args[:i], shared(args[i]), *args[i + 1:])
+    k, v, acc, ids = cache(2, 100, 1)
+    for kv in ((shared(k), v), (k, shared(v))):
+        with pytest.raises(ValueError):
+            G().cache_evict(90, 50, 100, *kv, acc, ids, acc.clone(), ids.clone(), G().new_cache_workspace(2, 100, 50))
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # a stream of views
 

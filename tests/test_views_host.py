@@ -143,3 +143,21 @@ def test_batch_defaults(lib):
     assert (c.n_kv_heads, c.max_q, c.max_own, c.causal, c.head_dim) == (8, 5, 7, 0, 64)
     c.q_stride = 4096
     assert b.copy_c().q_stride == 0  # each call has its own
+
+
+def test_tokens_that_share_memory_are_refused(lib):
+    # `_rows` takes host tensors for device -1, that of theirs: nothing is launched
+    from sparse_global_attention_view_b200 import views
+    x = torch.zeros(40, 2, 64, dtype=torch.bfloat16)
+    one = x[:1]
+    assert views._rows(x, 40, 2, -1, "x")[1] == 0 and views._rows(x[::2], 20, 2, -1, "x")[1] == 256
+    assert views._rows(one, 1, 2, -1, "x")[1] == 0 and views._rows(one.expand(1, 2, 64), 1, 2, -1, "x")[1] == 0
+    flat = x.flatten()
+    for bad in (one.expand(40, 2, 64), flat.as_strided((40, 2, 64), (64, 64, 1)), flat[:64].view(1, 1, 64).expand(40, 2, 64),
+                flat.as_strided((40, 2, 64), (120, 64, 1))):
+        for exact in (True, False):
+            with pytest.raises(ValueError):
+                views._rows(bad, 40, 2, -1, "x", exact)
+    for n in (40, 39):  # one head, a cache with room
+        with pytest.raises(ValueError):
+            views._rows(x[:1, :1].expand(40, 1, 64), n, 1, -1, "x", False)
