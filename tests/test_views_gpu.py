@@ -323,6 +323,48 @@ def test_a_nan_that_is_seen_shows(name):
         assert not out[:, G_:].isnan().any()
 
 
+@pytest.mark.parametrize("what", ["query", "lse"])
+@pytest.mark.parametrize("name", list(WAYS))
+def test_a_nan_that_is_seen_shows_in_the_account(name, what):
+    # every place of a row in a chunk of scores, in each view
+    x = make(*WAYS[name])
+    G_ = x["q"].shape[1] // x["kp"].shape[1]
+    batch, z = batch_of(x), exact_lse(x)
+    w = weigh(x, batch, z, None, 1.0)
+    P = x["kp"].shape[0]
+    for b, rows, cols in R.views(x["q_off"], x["own_off"]):
+        for i in range(rows.start, min(rows.stop, rows.start + 16)):
+            y, zz = x | dict(q=x["q"].clone()), z.clone()
+            if what == "query":
+                y["q"][i, 0] = float("nan")
+            else:
+                zz[i, 0] = float("nan")
+            got = weigh(y, batch, zz, None, 1.0)
+            nan = torch.zeros_like(w, dtype=torch.bool)
+            nan[0, :P] = True
+            nan[0, P + cols.start:P + cols.stop] = True
+            assert torch.equal(got.isnan(), nan), (b, i)
+            assert torch.equal(got[~nan], w[~nan]), (b, i)
+
+
+@pytest.mark.parametrize("name", ["poses", "mixed views", "long views"])
+def test_hidden_values_weigh_nothing(name):
+    # the largest finite values, behind what the causal mask lets a query see
+    x = make(*WAYS[name])
+    batch = batch_of(x, True)
+    good = attend(x, batch)
+    for b, rows, cols in R.views(x["q_off"], x["own_off"]):
+        hidden = min(rows.stop - rows.start - 1, cols.stop - cols.start)  # the first query does not see so many
+        y = x | dict(vo=x["vo"].clone())
+        for n in range(1, min(hidden, 20) + 1):
+            y["vo"][cols.stop - n] = 3.3e38
+        out, lse = attend(y, batch)
+        keep = torch.ones(out.shape[0], dtype=torch.bool)
+        keep[rows.stop - min(hidden, 20):rows.stop] = False
+        assert torch.equal(out[keep], good[0][keep]), b
+        assert torch.equal(lse, good[1])
+
+
 @pytest.mark.parametrize("strength", [0.0, 30.0, 3000.0])
 @pytest.mark.parametrize("name", list(WAYS))
 def test_flat_and_steep_scores(name, strength):
