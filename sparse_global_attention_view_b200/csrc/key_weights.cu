@@ -12,7 +12,8 @@
 //   warp 0       TMA producer: the item's key tiles (two sets of four, so the next
 //                item's keys arrive during this one) and a 5-stage ring of query tiles;
 //   warp 1       MMA issuer: for each query tile four products, one a key tile;
-//   warp 2       the query tile's -lse log2(e) into the ring (and TMEM allocation);
+//   warp 2       the query tile's -lse log2(e) into the ring, and which of its rows count
+//                for nothing (and TMEM allocation);
 //   warps 4-19   a warpgroup for each key tile: exponentials and sums.
 // While one warpgroup waits for its product the three others have the
 // exponential units busy: those bound it (half as many tensor flops an
@@ -24,8 +25,14 @@
 // keys; eight lanes hold a key, and after the dot products lane r takes the
 // exponential of row r.
 //
+// Rows that count for nothing (of no token, of a log sum of -infinity, hidden from a
+// key) are told by their place, not by an infinite score or log sum: one that holds
+// NaN or infinity, or meets an infinite key, would leave NaN otherwise.
+//
 // All sums are fp32: a tile's 128 terms in 8 chains, then tile after tile.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "exp2_poly.cuh"
 #include "views.h"
@@ -45,7 +52,9 @@ constexpr uint32_t kTile = 128 * 128;
 constexpr uint32_t OFF_K = 0;
 constexpr uint32_t OFF_Q = OFF_K + 2 * SLOTS * kTile;
 constexpr uint32_t OFF_L = OFF_Q + ST * kTile;
-constexpr uint32_t OFF_BAR = OFF_L + ST * 512;
+// a bit for each row of a query tile that counts for nothing, and whether there is one
+constexpr uint32_t OFF_NONE = OFF_L + ST * 512, OFF_SOME = OFF_NONE + ST * 16;
+constexpr uint32_t OFF_BAR = OFF_SOME + (ST * 4 + 7) / 8 * 8;
 constexpr uint32_t OFF_MISC = OFF_BAR + 256;
 constexpr uint32_t kSmemBytes = OFF_MISC + 64 + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -145,6 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sp + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sp + OFF_MISC + 4);
   float* sL = reinterpret_cast<float*>(sp + OFF_L);
+  uint32_t* sNone = reinterpret_cast<uint32_t*>(sp + OFF_NONE);
+  uint32_t* sSome = reinterpret_cast<uint32_t*>(sp + OFF_SOME);
 
   pdl_launch();
   const ViewDims& d = a.d;
@@ -269,19 +280,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = step % ST;
         const int tok0 = it.tok0 + i * MT;
         float v[4];
+        uint32_t none[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int row = u * 32 + lane, tl = row / d.G, tok = tok0 + tl;
           // rows of no token weigh nothing, as do queries that saw no key
-          v[u] = -CUDART_INF_F;
-          if (tl < MT && tok >= it.tok_lo && tok < it.tok_hi) {
-            const float z = a.lse[(long long)tok * d.H + it.hk * d.G + row - tl * d.G];
-            if (z != -CUDART_INF_F) v[u] = -z * 1.4426950408889634f;
-          }
+          float z = -CUDART_INF_F;
+          if (tl < MT && tok >= it.tok_lo && tok < it.tok_hi) z = a.lse[(long long)tok * d.H + it.hk * d.G + row - tl * d.G];
+          v[u] = -z * 1.4426950408889634f;
+          none[u] = __ballot_sync(0xffffffffu, z == -CUDART_INF_F);
         }
         if (step >= ST && !(ok = __all_sync(0xffffffffu, wait(B_QE + s, (step / ST - 1) & 1)))) break;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) sL[s * 128 + u * 32 + lane] = v[u];
+        for (int u = 0; u < 4; ++u) {
+          sL[s * 128 + u * 32 + lane] = v[u];
+          if (lane == 0) sNone[s * 4 + u] = none[u];
+        }
+        if (lane == 0) sSome[s] = none[0] | none[1] | none[2] | none[3];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_LF + s));
       }
@@ -313,56 +328,68 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           sf ^= 1;
           fence_after_sync();
-          // rows [lo, hi) of the tile see this key
+          // rows before lo do not see this key, and there are none from hi on
           const int tok0 = it.tok0 + i * MT;
-          const int lo = max(max(it.tok_lo, it.see0 + r) - tok0, 0) * d.G;
+          const int lo = (max(it.see0 + r, tok0) - tok0) * d.G;
           const int hi = it.tok_hi - tok0 >= MT ? 128 : (it.tok_hi - tok0) * d.G;
-          // rows behind the last query that there is are zeros, and weigh nothing by
-          // their log sum; others may hold anything
-          const bool whole = __all_sync(0xffffffffu, lo == 0 && (hi == 128 || it.tok_hi == d.n_q));
+          const bool whole = __all_sync(0xffffffffu, lo == 0 && sSome[s] == 0u);
           const float4* nl = reinterpret_cast<const float4*>(sL + s * 128);
           uint64_t ps[4] = {0ull, 0ull, 0ull, 0ull};
           uint32_t sv[32];
-          auto chunk = [&](int c) {
-            if (!whole) {
-#pragma unroll
-              for (int u = 0; u < 32; ++u)
-                if (32 * c + u < lo || 32 * c + u >= hi) sv[u] = __float_as_uint(-CUDART_INF_F);
-            }
+          // SOME: without the columns whose bit is set in `skip`
+          auto chunk = [&](int c, auto some, uint32_t skip) {
+            constexpr bool SOME = decltype(some)::value;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               const float4 z = nl[8 * c + u];
 #pragma unroll
               for (int w = 0; w < 2; ++w) {
                 const int k = 4 * u + 2 * w;
-                const uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2p,
-                                           w ? f2_pack(z.z, z.w) : f2_pack(z.x, z.y));
-                uint64_t p2;
-                if (((2 * u + w) & 7) >= 8 - kPolyOf8) {
-                  p2 = exp2_poly2(x2);
-                } else {
-                  float x0, x1;
-                  f2_unpack(x2, x0, x1);
-                  p2 = f2_pack(exp2_mufu(x0), exp2_mufu(x1));
+                uint64_t x2 = f2_fma(f2_pack(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2p,
+                                     w ? f2_pack(z.z, z.w) : f2_pack(z.x, z.y));
+                float x0, x1;
+                f2_unpack(x2, x0, x1);
+                if (SOME) {
+                  if (skip >> k & 1) x0 = -CUDART_INF_F;
+                  if (skip >> (k + 1) & 1) x1 = -CUDART_INF_F;
+                  x2 = f2_pack(x0, x1);
                 }
+                const uint64_t p2 = ((2 * u + w) & 7) >= 8 - kPolyOf8 ? exp2_poly2(x2) : f2_pack(exp2_mufu(x0), exp2_mufu(x1));
                 ps[(2 * u + w) & 3] = f2_add(ps[(2 * u + w) & 3], p2);
               }
             }
           };
-          // as far as there are queries (a rolled loop: registers to overlap the
+          // as far as there are queries (rolled loops: registers to overlap the
           // exponentials in, and little code; 943 us at 5496 queries and 46716 keys of
-          // 16 heads against 1159 with the next load in flight)
-          const int chunks = max(1, (min(hi, 128) + 31) >> 5);
-#pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
+          // 16 heads against 1159 with the next load in flight; a loop of its own for
+          // tiles whose rows all count, 896 against 934 with both in one)
+          auto load = [&](int c, bool last) {
             tmem_ld32(s_addr + 32 * c, sv);
             tmem_wait_ld();
-            if (c == chunks - 1) {
+            if (last) {
               fence_before_sync();
               __syncwarp();
               if (lane == 0) mbar_arrive(bar(B_SE + t));
             }
-            chunk(c);
+          };
+          if (whole) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              load(c, c == 3);
+              chunk(c, std::false_type{}, 0u);
+            }
+          } else {
+            const int chunks = max(1, (min(hi, 128) + 31) >> 5);
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+              load(c, c == chunks - 1);
+              const int before = lo - 32 * c;
+              const uint32_t skip = sNone[s * 4 + c] | (before >= 32 ? 0xffffffffu : before > 0 ? (1u << before) - 1 : 0u);
+              if (__any_sync(0xffffffffu, skip != 0u))
+                chunk(c, std::true_type{}, skip);
+              else
+                chunk(c, std::false_type{}, 0u);
+            }
           }
           const uint64_t p01 = f2_add(f2_add(ps[0], ps[1]), f2_add(ps[2], ps[3]));
           float p0, p1;
@@ -465,11 +492,8 @@ __global__ void __launch_bounds__(256)
   }
   // lane e looks after row e
   const int my_tok = e / d.G;
-  float nl = -CUDART_INF_F;
-  if (e < rows) {
-    const float z = a.lse[(long long)my_tok * d.H + hk * d.G + e - my_tok * d.G];
-    if (z != -CUDART_INF_F) nl = -z * 1.4426950408889634f;
-  }
+  const float z = e < rows ? a.lse[(long long)my_tok * d.H + hk * d.G + e - my_tok * d.G] : -CUDART_INF_F;
+  const float nl = -z * 1.4426950408889634f;
   int tok_lo = max(d.q_off[0], 0), tok_hi = min(d.q_off[d.B], d.n_q);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
@@ -497,7 +521,7 @@ __global__ void __launch_bounds__(256)
       s += __shfl_xor_sync(0xffffffffu, s, 4);
       if (i == e) mine = s;
     }
-    float p = e < rows && my_tok >= tok_lo && my_tok < tok_hi ? exp2_mufu(fmaf(mine, d.c2, nl)) : 0.f;
+    float p = z != -CUDART_INF_F && my_tok >= tok_lo && my_tok < tok_hi ? exp2_mufu(fmaf(mine, d.c2, nl)) : 0.f;
     p += __shfl_xor_sync(0xffffffffu, p, 1);
     p += __shfl_xor_sync(0xffffffffu, p, 2);
     p += __shfl_xor_sync(0xffffffffu, p, 4);

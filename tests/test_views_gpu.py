@@ -328,7 +328,6 @@ def test_a_nan_that_is_seen_shows(name):
 def test_a_nan_that_is_seen_shows_in_the_account(name, what):
     # every place of a row in a chunk of scores, in each view
     x = make(*WAYS[name])
-    G_ = x["q"].shape[1] // x["kp"].shape[1]
     batch, z = batch_of(x), exact_lse(x)
     w = weigh(x, batch, z, None, 1.0)
     P = x["kp"].shape[0]
@@ -345,6 +344,64 @@ def test_a_nan_that_is_seen_shows_in_the_account(name, what):
             nan[0, P + cols.start:P + cols.stop] = True
             assert torch.equal(got.isnan(), nan), (b, i)
             assert torch.equal(got[~nan], w[~nan]), (b, i)
+
+
+# the ways, and rows of a tile that are no token's: groups that do not divide 128, tokens that do not fill the tile
+ACCOUNTS = WAYS | {"groups of 3": (6, 2, [50, 7, 100], [33, 129, 100], 257), "groups of 5, short": (5, 1, [1, 2, 1], [33, 129, 100], 257)}
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", list(ACCOUNTS))
+def test_queries_without_a_log_sum_count_for_nothing(name, bad):
+    x = make(*ACCOUNTS[name])
+    for b, rows, cols in R.views(x["q_off"], x["own_off"]):
+        for i in range(rows.start, min(rows.stop, rows.start + 16)):
+            z = exact_lse(x)
+            z[i] = R.NEG
+            y = x | dict(q=x["q"].clone())
+            y["q"][i] = bad
+            batch = batch_of(x)
+            got = weigh(y, batch, z, None, 1.0)
+            # finite in the place of what counts for nothing: the same bits
+            assert not got.isnan().any() and torch.equal(got, weigh(x, batch, z, None, 1.0)), (b, i)
+    # nobody counts at all
+    y, z = x | dict(q=torch.full_like(x["q"], bad)), torch.full_like(z, R.NEG)
+    assert (weigh(y, batch, z, None, 1.0) == 0).all()
+
+
+@pytest.mark.parametrize("name", list(ACCOUNTS))
+def test_queries_that_do_not_see_a_key_leave_its_account(name):
+    # causal: the first query of a view holds NaN, in its values or its log sum
+    x = make(*ACCOUNTS[name])
+    batch, z0 = batch_of(x, True), exact_lse(x, True)
+    good = weigh(x, batch, z0, None, 1.0)
+    P = x["kp"].shape[0]
+    for b, rows, cols in R.views(x["q_off"], x["own_off"]):
+        see = R.seen(rows.stop - rows.start, cols.stop - cols.start, True, DEV)[0]
+        for y, z in ((x | dict(q=x["q"].clone()), z0), (x, z0.clone())):
+            (z if y is x else y["q"])[rows.start] = float("nan")
+            got = weigh(y, batch, z, None, 1.0)
+            nan = torch.zeros_like(got, dtype=torch.bool)
+            nan[:, :P] = True
+            nan[:, P + cols.start:P + cols.stop] = see
+            assert torch.equal(got.isnan(), nan), b
+            assert torch.equal(got[~nan], good[~nan]), b
+
+
+@pytest.mark.parametrize("name", list(ACCOUNTS))
+def test_an_infinite_key_that_nobody_looks_at(name):
+    # every score with it is -infinity: a weight of 0, whatever lies in a tile's other rows
+    x = make(*ACCOUNTS[name])
+    x["q"] = x["q"].abs()
+    P = x["kp"].shape[0]
+    cols = [0, 100, P - 1]
+    for t, at in ((x["kp"], cols), (x["ko"], [0, x["ko"].shape[0] - 1])):
+        t[at] = float("-inf")
+    z = exact_lse(x)
+    assert z.isfinite().all()
+    got = weigh(x, batch_of(x), z, None, 1.0)
+    assert (got[:, cols + [P, -1]] == 0).all()
+    assert_weights(x, got, z, None, 1.0)
 
 
 @pytest.mark.parametrize("name", ["poses", "mixed views", "long views"])
