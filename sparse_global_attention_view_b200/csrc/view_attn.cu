@@ -1177,6 +1177,11 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
   }
   if (p.parts > 0 || (!p.packed && !p.aligned)) {
     const long long blocks = ((long long)d.n_q * d.H * 8 + 255) / 256;
+    if (p.parts == 0) {
+      // no keys at all: the call's only kernel
+      merge_kernel<<<(unsigned)blocks, 256, 0, st>>>(d, 0, part_o, part_lse, out, lse, err);
+      return cudaGetLastError();
+    }
     return launch_second(merge_kernel, dim3((unsigned)blocks), 256, st, d, p.parts, (const float*)part_o,
                          (const float*)part_lse, out, lse, err);
   }

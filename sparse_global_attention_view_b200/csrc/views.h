@@ -76,9 +76,12 @@ cudaError_t allow_smem(F* kernel, int bytes, std::atomic<unsigned long long>* do
 }
 
 // A second kernel of a call: launched while the first one still runs, so that its
-// start is not waited for.  The first kernel calls pdl_launch() at its start, the
-// second one pdl_wait() before it touches memory: it goes on when the first one has
-// ended and its writes are visible.
+// start is not waited for.  The first kernel, launched in the ordinary way, calls
+// pdl_launch() at its start; the second one calls pdl_wait() before it reads what the
+// first one writes or writes what the first one touches: it goes on when the first one
+// has ended and its writes are visible.  What was written before the call (offsets,
+// queries, keys) may be read ahead of that, since the first kernel began behind it: so
+// a call's only kernel is never launched this way.
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 template <typename... P, typename... A>

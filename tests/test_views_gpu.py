@@ -681,6 +681,27 @@ def test_offsets_are_looked_at_where_no_own_key_is_expected(H, ql, prefix):
     assert (w == 0).all()  # nobody looked
 
 
+def test_offsets_written_by_the_kernel_before():
+    # a batch without any key is one kernel; its offsets are what the call before leaves: log sums of 0 are the number 0
+    n = 200_000
+    x = make(1, 1, [n], [0], 1)
+    x["q"] = torch.zeros_like(x["q"])
+    batch, ws = batch_of(x), G().new_view_workspace(batch_of(x))
+    off, out, lse = ints([0, n]), torch.empty_like(x["q"]), torch.empty(n, 1, device=DEV)
+    none = G().ViewBatch(n_views=1, n_q=300, n_own=0, n_prefix=0, n_heads=1)
+    ws2, out2, lse2 = G().new_view_workspace(none), torch.full((300, 1, 64), 7.0, device=DEV).bfloat16(), torch.full((300, 1), 7.0, device=DEV)
+    for _ in range(20):
+        lse.view(torch.int32).fill_(1 << 30)
+        G().prefix_attn(batch, x["q"], x["kp"], x["vp"], None, None, off, ints([0, 0]), out, lse, ws)
+        late = lse.view(torch.int32).flatten()[-2:]
+        G().prefix_attn(none, x["q"][:300], None, None, None, None, late, ints([0, 0]), out2, lse2, ws2)
+        G().check_device_error(ws2)
+        assert (late == 0).all() and (out2 == 7).all() and (lse2 == 7).all()
+    off2 = ints([0, 300])
+    G().prefix_attn(none, x["q"][:300], None, None, None, None, off2, ints([0, 0]), out2, lse2, ws2)
+    assert (out2 == 0).all() and (lse2 == R.NEG).all()
+
+
 def test_waits_that_run_out():
     # the hardware itself holds a waiting thread for a microsecond or so before the limit is looked at, so this takes
     # waits that are longer: the copies' on a full ring of key or query tiles
