@@ -242,8 +242,14 @@ class ViewCache:
         self._ws = None
 
     def _workspace(self, n_bytes: int) -> torch.Tensor:
-        if self._ws is None or self._ws.numel() < n_bytes:
+        old = self._ws
+        if old is None or old.numel() < n_bytes:
             self._ws = _new_workspace(n_bytes, self.k.device, None)
+            if old is not None:
+                # errors that nobody has asked for yet
+                self._ws[:WS_HEADER_BYTES].copy_(old[:WS_HEADER_BYTES])
+                # earlier steps may have used it on another stream than the one it came from
+                old.record_stream(torch.cuda.current_stream(old.device))
         return self._ws
 
     def step(self, q, k, v, lens=None, decay: float = 1.0) -> torch.Tensor:

@@ -804,3 +804,20 @@ def test_a_stream_of_views(H, Hk):
             assert all((c.ids[:, :300] == i).any(1).all() for i in range(full - 50, full))
     with pytest.raises(ValueError):
         c.step(*(torch.zeros(500, h, 64, dtype=torch.bfloat16, device=DEV) for h in (H, Hk, Hk)))
+
+
+def test_errors_outlive_a_workspace():
+    c = G().ViewCache(20_000, 2)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    step = lambda n: c.step(*(torch.randn(n, 2, 64, generator=g, device=DEV).bfloat16() for _ in range(3)))  # noqa: E731
+    step(40)
+    small = c._ws.numel()
+    c._ws[:4].view(torch.int32)[0] = 2  # what a kernel leaves whose check failed
+    step(6000)
+    assert c._ws.numel() > small
+    step(300)
+    with pytest.raises(G().GsaError) as e:
+        c.check_device_error()
+    assert e.value.status == 6
+    step(3)
+    c.check_device_error()  # reported once
