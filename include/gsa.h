@@ -391,15 +391,15 @@ gsa_status gsa_noalloc_check_device_error(void* stream);
  * Infinite or NaN keys and values of one view never reach another view's rows.
  */
 typedef struct {
-  int32_t n_views;     /* B >= 1 */
+  int32_t n_views;     /* B >= 1; B * max(1, ceil(max_q / (2 * floor(128 * Hk / H)))) <= 2^25 - 1 */
   int32_t n_heads;     /* H in [1, 128] query heads */
   int32_t n_kv_heads;  /* Hk >= 1, divides H */
   int32_t head_dim;    /* only 64 is built */
-  int32_t n_q;         /* query tokens that q and out hold, >= 0 */
+  int32_t n_q;         /* query tokens that q and out hold, in [0, 2^24 - 9] */
   int32_t n_own;       /* own tokens that k_own and v_own hold, >= 0 */
-  int32_t n_prefix;    /* cached tokens, >= 0 */
-  int32_t max_q;       /* most queries of a view, in [0, n_q] */
-  int32_t max_own;     /* most own tokens of a view, in [0, n_own] */
+  int32_t n_prefix;    /* cached tokens, >= 0; n_prefix + n_own <= 2^31 - 1025 */
+  int32_t max_q;       /* most queries of a view, in [0, n_q]: what the work is laid out for, so */
+  int32_t max_own;     /* the closer the faster; and most own tokens of a view, in [0, n_own] */
   int32_t causal;      /* 0: a query sees all tokens of its view; 1: the last query of a view
                           sees all its own tokens, each query before it one token less */
   float scale;         /* softmax scale; 0 means 1/sqrt(64) */
@@ -444,6 +444,7 @@ gsa_status prefix_attn(const gsa_view_batch* batch, const gsa_bf16* q, const gsa
  * way to have a token never evicted.  A query whose lse is -infinity counts for
  * nothing.  Slots of own tokens that belong to no view are not written.
  * Sums are added in a fixed order: equal calls give equal bits.
+ * Hk * (ceil(n_prefix / 512) + B * ceil(max_own / 512)) is at most 2^31 - 1025.
  */
 gsa_status key_weights(const gsa_view_batch* batch, const gsa_bf16* q, const gsa_bf16* k_prefix,
                        const gsa_bf16* k_own, const int32_t* q_off, const int32_t* own_off, const float* lse,

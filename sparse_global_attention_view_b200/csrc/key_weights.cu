@@ -630,9 +630,12 @@ WeightsPlan weights_plan(const ViewDims& d) {
     const double longest = (per_p > ceil_div(tiles_o, so) ? per_p : ceil_div(tiles_o, so)) + 2.0;
     const double cost = work / 148.0 + (items > 148.0 ? 0.5 : 1.0) * longest + (s > 1 ? 6.0 : 0.0);
     if (s == 1 || cost < best) {
+      WeightsPlan x = p;
+      x.split_prefix = s;
+      x.split_own = so;
+      if (s > 1 && weights_items(d, x) > kMostItems) break;
       best = cost;
-      p.split_prefix = s;
-      p.split_own = so;
+      p = x;
     }
   }
   return p;
@@ -668,9 +671,7 @@ cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf
   a.m_units = 0xffffffffu / (uint32_t)(p.prefix_units > 0 ? p.prefix_units : 1);
   a.m_split = 0xffffffffu / (uint32_t)p.split_prefix;
   a.m_tok = 0xffffffffu / (uint32_t)MT;
-  const long long items = ((long long)p.prefix_units * p.split_prefix + (long long)d.B * p.own_units * p.split_own) * d.Hk;
-  if (items > 0x7fffffffLL - 1024) return cudaErrorInvalidValue;
-  a.n_items = (int)items;
+  a.n_items = (int)weights_items(d, p);
   if (a.n_items > 0) {
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = allow_smem(key_weights_kernel, (int)kSmemBytes, &done);

@@ -47,6 +47,12 @@ struct WeightsPlan {
   int split_prefix, split_own;    // query ranges of an item
 };
 WeightsPlan weights_plan(const ViewDims& d);
+// Work items of the plan: a 32-bit number of them, and the grid's stride more, is what
+// the kernel counts to.
+inline long long weights_items(const ViewDims& d, const WeightsPlan& p) {
+  return ((long long)p.prefix_units * p.split_prefix + (long long)d.B * p.own_units * p.split_own) * d.Hk;
+}
+constexpr long long kMostItems = 0x7fffffffLL - 1024;
 
 cudaError_t launch_key_weights(const ViewDims& d, const WeightsPlan& p, const bf16* q, const bf16* kp, const bf16* ko,
                                const float* lse, const float* acc, long long acc_stride, float* acc_out,

@@ -40,7 +40,9 @@ gsa_status make_view_dims(const gsa_view_batch* b, ViewDims* d) {
   // slots of the cache after an append, tile starts and grids are int32
   constexpr long long most = INT32_MAX - 1024;
   if ((long long)b->n_prefix + b->n_own > most || b->n_q > most / 128) return GSA_ERR_INVALID_ARG;
-  if ((long long)b->n_views * ((b->max_q + 127LL) / 128 + 1) * 64 * 128 > INT32_MAX) return GSA_ERR_INVALID_ARG;
+  // so is the grid of the views' row tiles, two a block, in at most 64 key ranges
+  const long long unit = 2 * (128 / (b->n_heads / b->n_kv_heads)), units = (b->max_q + unit - 1) / unit;
+  if (b->n_views * (units > 1 ? units : 1) > INT32_MAX / 64) return GSA_ERR_INVALID_ARG;
   ViewDims t = {};
   t.B = b->n_views;
   t.H = b->n_heads;
@@ -180,6 +182,7 @@ gsa_status key_weights(const gsa_view_batch* batch, const gsa_bf16* q, const gsa
       overlap(acc, span(d.Hk, d.n_prefix, acc_stride), acc_out, span(d.Hk, keys, acc_out_stride)))
     return GSA_ERR_INVALID_ARG;
   const gsa::WeightsPlan p = gsa::weights_plan(d);
+  if (gsa::weights_items(d, p) > gsa::kMostItems) return GSA_ERR_INVALID_ARG;
   const WeightsLayout l = weights_layout(d, p);
   if (ws_bytes < l.total) return GSA_ERR_WORKSPACE;
   d.q_off = q_off;

@@ -20,7 +20,11 @@ from .api import BF16, F32, I32, WS_HEADER_BYTES, check_device_error
 
 @dataclass(frozen=True)
 class ViewBatch:
-    """Sizes of a batch of views that share a cache (``gsa_view_batch``)."""
+    """Sizes of a batch of views that share a cache (``gsa_view_batch``).
+
+    The work is laid out for n_views views of max_q queries and max_own own tokens: the defaults fit any batch, and
+    take longer where there are many views.
+    """
 
     n_views: int
     n_q: int

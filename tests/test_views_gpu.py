@@ -702,6 +702,38 @@ def test_offsets_written_by_the_kernel_before():
     assert (out2 == 0).all() and (lse2 == R.NEG).all()
 
 
+def test_many_views_of_unknown_length():
+    # the default sizes: every view may hold all tokens
+    x = make(1, 1, [10 - i % 3 for i in range(2000)], [11 - i % 4 for i in range(2000)], 300)
+    batch = batch_of(x, max_q=-1, max_own=-1)
+    assert batch.c().max_q == x["q"].shape[0]
+    out, lse = attend(x, batch)
+    assert_attend(x, out, lse)
+    z = exact_lse(x)
+    assert_weights(x, weigh(x, batch, z, None, 1.0), z, None, 1.0)
+
+
+def test_more_views_than_a_short_number():
+    n, P = 140_000, 40
+    x = make(1, 1, [1] * n, [1] * n, P)
+    batch = batch_of(x)
+    out, lse = attend(x, batch)
+    q, kp, vp, ko, vo = (x[t][:, 0].double() for t in ("q", "kp", "vp", "ko", "vo"))
+    s = torch.cat((q @ kp.T, (q * ko).sum(1, keepdim=True)), 1) * 0.125
+    z = torch.logsumexp(s, 1)
+    p = (s - z[:, None]).exp()
+    v = torch.cat((vp, vo[:1] * 0))  # own values apart: one for each query
+    o = p @ v + p[:, P:] * vo
+    # roundings of the weights and the result to bf16; sums, logits and exponentials of 41 terms are within 2e-5
+    size = p[:, :P] @ vp.abs() + p[:, P:] * vo.abs()
+    assert ((out[:, 0].double() - o).abs() <= (R.U16 + 2e-5) * 1.01 * size + R.U16 * 1.01 * o.abs()).all()
+    assert ((lse[:, 0].double() - z).abs() <= 2e-5 * (1 + z.abs())).all()
+    w = weigh(x, batch, lse, None, 1.0)[0].double()
+    assert ((w[P:] - p[:, P]).abs() <= 1e-4 * p[:, P]).all()
+    # 140000 terms: at most n / 64 + 64 roundings of a sum on the way
+    assert ((w[:P] - p[:, :P].sum(0)).abs() <= (1e-4 + (n / 64 + 64) * R.U32) * p[:, :P].sum(0)).all()
+
+
 def test_waits_that_run_out():
     # the hardware itself holds a waiting thread for a microsecond or so before the limit is looked at, so this takes
     # waits that are longer: the copies' on a full ring of key or query tiles

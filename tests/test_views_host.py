@@ -161,3 +161,25 @@ def test_tokens_that_share_memory_are_refused(lib):
     for n in (40, 39):  # one head, a cache with room
         with pytest.raises(ValueError):
             views._rows(x[:1, :1].expand(40, 1, 64), n, 1, -1, "x", False)
+
+
+def test_many_views_are_fine(lib):
+    frame = 1374
+    for kw in (dict(n_views=200, n_q=200 * frame, n_own=200 * frame, max_q=200 * frame, max_own=200 * frame),  # the defaults
+               dict(n_views=1000, n_q=1000 * frame, n_own=1000 * frame, max_q=1000 * frame, max_own=1000 * frame, n_kv_heads=16),
+               dict(n_views=131072, max_q=1), dict(n_views=5_000_000, n_q=5_000_000, max_q=1, n_own=5_000_000, max_own=1),
+               dict(n_views=2 ** 25 - 1, max_q=64, max_own=0), dict(n_views=2 ** 24 - 1, max_q=65, max_own=0)):
+        st, n = size(lib, batch(**kw))
+        assert st == 0 and n >= 256, kw
+    for kw in (dict(n_views=2 ** 25, max_q=64), dict(n_views=2 ** 24, max_q=65), dict(n_views=2 ** 25, max_q=0),
+               dict(n_views=2 ** 24, n_heads=128, n_kv_heads=1, max_q=3)):
+        assert size(lib, batch(**kw))[0] == 1, kw
+
+
+def test_accounts_of_too_many_views_are_refused(lib):
+    # views, heads and items of 512 own tokens: more of them than 32 bits count
+    args = [FAKE] * 6 + [None, 0, FAKE << 20, BIG >> 4, 1.0, FAKE, 1 << 62, None]
+    for kw in (dict(n_views=2 ** 27 // 16, n_kv_heads=16, n_own=20 * 512, max_own=16 * 512), dict(n_views=2 ** 24, max_q=64, max_own=100, n_kv_heads=128, n_heads=128)):
+        b = batch(**kw)
+        assert size(lib, b)[0] == 0, kw
+        assert lib.key_weights(ctypes.byref(b), *args) == 1, kw
