@@ -130,7 +130,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tok0 = (long long)unit * unit_tok;
     tok_lo = max(d.q_off[0], 0);
     tok_end = min(d.q_off[d.B], d.n_q);
-    if (tok0 >= tok_end || tok0 + unit_tok <= tok_lo) return;
+    if (tok0 >= tok_end || tok0 + unit_tok <= tok_lo) {
+      // a launch that reads no own keys still reports offsets that promise some: a block
+      // behind the rows (checks elsewhere in the kernel cost its softmax registers: 1325
+      // us at 5496 x 42594 x 16 heads against 1306)
+      if (a.check_views && blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) check_views(d, tid, kThreads, a.err);
+      return;
+    }
   }
   const int last_row = (int)min(tok0 + unit_tok, (long long)tok_end) - 1;
   // own keys seen by at least one of the rows
@@ -290,9 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(bar(B_DRAIN + w), 0, &never, a.err);
       }
     }
-  } else if (warp == 2) {
-    // a launch that reads no own keys still reports offsets that promise some
-    if (a.check_views && blockIdx.x == 0 && blockIdx.y == 0) check_views(d, lane, 32, a.err);
   } else if (warp >= 4) {
     // ---------------- softmax of stream x, one thread a row ----------------
     const int x = (warp - 4) >> 2, w = x >> 1, half = x & 1;
@@ -1139,7 +1142,7 @@ cudaError_t launch_prefix_attn(const ViewDims& d, const ViewPlan& p, const bf16*
       a.n_split = p.split_packed;
       a.units_per_view = 0;
       a.part0 = 0;
-      const dim3 grid((unsigned)(ceil_div(d.n_q, 2 * MT) * a.n_split), (unsigned)d.Hk);
+      const dim3 grid((unsigned)(ceil_div(d.n_q, 2 * MT) * a.n_split + (a.check_views ? 1 : 0)), (unsigned)d.Hk);
       view_attn_kernel<<<grid, kThreads, kSmemBytes, st>>>(mq, mkp, mvp, mko, mvo, a);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;

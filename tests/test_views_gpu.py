@@ -702,6 +702,22 @@ def test_offsets_written_by_the_kernel_before():
     assert (out2 == 0).all() and (lse2 == R.NEG).all()
 
 
+@pytest.mark.parametrize("prefix", [1, 100, 6000])
+def test_offsets_are_looked_at_behind_a_padded_front(prefix):
+    # the first tiles hold no view's rows
+    x = make(2, 2, [300, 40], [0, 0], prefix)
+    x["q"] = torch.cat((torch.full((700, 2, 64), float("nan"), dtype=torch.bfloat16, device=DEV), x["q"]))
+    x["q_off"] = [700 + a for a in x["q_off"]]
+    batch = batch_of(x)
+    out, lse = attend(x, batch)
+    assert_attend(x, out, lse)
+    for case in (dict(own_off=[0, 0, 40]), dict(q_off=[700, 650, 1040]), dict(q_off=[1040, 1040, 700]), dict(q_off=[0, -1, -5])):
+        for call in (lambda y: attend(y, batch), lambda y: weigh(y, batch, lse, None, 1.0)):
+            with pytest.raises(G().GsaError) as e:
+                call(x | case)
+            assert e.value.status == 6, case
+
+
 def test_many_views_of_unknown_length():
     # the default sizes: every view may hold all tokens
     x = make(1, 1, [10 - i % 3 for i in range(2000)], [11 - i % 4 for i in range(2000)], 300)
