@@ -18,6 +18,9 @@ from ._lib import GsaCache, GsaViewBatch, check, load
 from .api import BF16, F32, I32, WS_HEADER_BYTES, check_device_error
 
 
+_LEAST, _MOST = -2 ** 31, 2 ** 31 - 1  # ctypes would cut off what is larger
+
+
 @dataclass(frozen=True)
 class ViewBatch:
     """Sizes of a batch of views that share a cache (``gsa_view_batch``).
@@ -40,6 +43,9 @@ class ViewBatch:
     wait_limit_ns: int = 0
 
     def c(self) -> GsaViewBatch:
+        for name, x in vars(self).items():
+            if isinstance(x, int) and not _LEAST <= x <= _MOST:
+                raise ValueError(f"{name} = {x} does not fit 32 bits")
         return GsaViewBatch(self.n_views, self.n_heads, self.n_kv_heads or self.n_heads, self.head_dim, self.n_q,
                             self.n_own, self.n_prefix, self.n_q if self.max_q < 0 else self.max_q,
                             self.n_own if self.max_own < 0 else self.max_own, int(self.causal), float(self.scale),
@@ -188,14 +194,19 @@ def key_weights(batch: ViewBatch, q, k_prefix, k_own, q_off, own_off, lse, acc, 
          _flat(lse, F32, (n_q, H), dev, "lse"), pacc, acc_stride, pout, out_stride, decay, pws, ws_bytes)
 
 
-def _cache(n_kv_heads: int, n_tokens: int, n_keep: int, recent_from: int = 0) -> GsaCache:
-    return GsaCache(n_kv_heads, 64, n_tokens, n_keep, recent_from, 0, 0, n_tokens)
+def _cache(n_kv_heads: int, n_tokens: int, n_keep: int, recent_from: int, k_stride: int, v_stride: int,
+           w_stride: int) -> GsaCache:
+    if not (_LEAST <= n_kv_heads <= _MOST and _LEAST <= n_tokens <= _MOST and _LEAST <= n_keep <= _MOST
+            and _LEAST <= recent_from <= _MOST):
+        raise ValueError(f"n_kv_heads, n_tokens, n_keep or recent_from of {(n_kv_heads, n_tokens, n_keep, recent_from)} "
+                         "does not fit 32 bits")
+    return GsaCache(n_kv_heads, 64, n_tokens, n_keep, recent_from, k_stride, v_stride, w_stride)
 
 
 def cache_workspace_size(n_kv_heads: int, n_tokens: int, n_keep: int) -> int:
     n = ctypes.c_size_t()
-    check(load().cache_workspace_size(ctypes.byref(_cache(n_kv_heads, n_tokens, n_keep)), ctypes.byref(n)),
-          "cache_workspace_size")
+    b = _cache(n_kv_heads, n_tokens, n_keep, 0, 0, 0, n_tokens)
+    check(load().cache_workspace_size(ctypes.byref(b), ctypes.byref(n)), "cache_workspace_size")
     return n.value
 
 
@@ -222,7 +233,7 @@ def cache_evict(n_tokens: int, n_keep: int, recent_from: int, k, v, acc, ids, ac
     pio, s3 = _table(ids_out, I32, Hk, n_tokens, dev, "ids_out")
     if Hk > 1 and not stride == s1 == s2 == s3:
         raise ValueError(f"acc, ids, acc_out and ids_out must have one row stride, got {(stride, s1, s2, s3)}")
-    b = GsaCache(Hk, 64, n_tokens, n_keep, recent_from, k_stride, v_stride, stride)
+    b = _cache(Hk, n_tokens, n_keep, recent_from, k_stride, v_stride, stride)
     _run(load().cache_evict, "cache_evict", dev, stream, ctypes.byref(b), pk, pv, pa, pi, pao, pio, pws, ws_bytes)
 
 

@@ -794,6 +794,16 @@ def test_python_refusals():
         G().cache_evict(101, 50, 100, k, v, acc, ids, torch.empty_like(acc), torch.empty_like(ids), evict_ws)
 
 
+def test_a_token_number_that_does_not_fit_is_refused():
+    k, v, acc, ids = cache(2, 100, 1)
+    before = k.clone()
+    for keep, recent_from in ((50, 2 ** 31), (2 ** 32 + 50, 100), (50, -2 ** 31 - 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            G().cache_evict(100, keep, recent_from, k, v, acc, ids, acc.clone(), ids.clone(), G().new_cache_workspace(2, 100, 50))
+    assert torch.equal(k, before)
+    assert_evicted(k, v, acc, ids, 50, 2 ** 31 - 1, *evict(k, v, acc, ids, 50, 2 ** 31 - 1))
+
+
 def test_expanded_tensors_are_refused():
     x = make(2, 2, [5], [5], 300)
     batch = batch_of(x)

@@ -183,3 +183,21 @@ def test_accounts_of_too_many_views_are_refused(lib):
         b = batch(**kw)
         assert size(lib, b)[0] == 0, kw
         assert lib.key_weights(ctypes.byref(b), *args) == 1, kw
+
+
+def test_numbers_beyond_32_bits_are_refused(lib):
+    import sparse_global_attention_view_b200 as G
+    from sparse_global_attention_view_b200 import views
+    base = dict(n_views=1, n_q=5, n_own=7, n_prefix=3, n_heads=8)
+    for name in ("n_views", "n_q", "n_own", "n_prefix", "n_heads", "n_kv_heads", "max_q", "max_own", "wait_limit_ns"):
+        for x in (2 ** 32 + base.get(name, 5), -2 ** 32 + 5):
+            with pytest.raises(ValueError, match="32 bits"):
+                G.view_workspace_size(G.ViewBatch(**base | {name: x}))
+    assert G.view_workspace_size(G.ViewBatch(**base)) >= 256
+    # n_keep of 2^32 + 5 is not 5, and recent_from of 2^31 (no token is so recent) not -2^31 (all are)
+    for args in ((4, 100, 2 ** 32 + 5, 0), (4, 100, 50, 2 ** 31), (4, 100, 50, -2 ** 31 - 1), (4, 2 ** 32 + 100, 50, 0), (2 ** 32 + 4, 100, 50, 0)):
+        with pytest.raises(ValueError, match="32 bits"):
+            views._cache(*args, 0, 0, 100)
+    with pytest.raises(ValueError, match="32 bits"):
+        G.cache_workspace_size(4, 100, 2 ** 32 + 5)
+    assert views._cache(4, 100, 50, 2 ** 31 - 1, 0, 0, 100).recent_from == 2 ** 31 - 1
