@@ -241,7 +241,8 @@ class ViewCache:
     """Keys and values of the views seen so far, with their account: the operators in the order of a stream of views.
 
     ``step`` attends a batch of views to the cache and to their own tokens, adds up who was looked at and appends the
-    tokens; ``evict`` shrinks the cache.  Everything runs on the current stream of ``device``.
+    tokens; ``evict`` shrinks the cache.  Everything runs on the current stream of ``device``.  Tokens are numbered in
+    the order of their coming, up to 2^31 - 1 of them; a ``step`` that is refused leaves the cache as it was.
     """
 
     def __init__(self, capacity: int, n_heads: int, n_kv_heads: int = 0, device="cuda", scale: float = 0.0):
@@ -272,10 +273,12 @@ class ViewCache:
         own tokens, q [n, H, 64], k and v [n, Hk, 64]; then the tokens join the cache."""
         n = q.shape[0]
         lens = [n] if lens is None else list(lens)
-        if sum(lens) != n:
-            raise ValueError(f"the views have {sum(lens)} tokens, q has {n}")
+        if not lens or min(lens) < 0 or sum(lens) != n:
+            raise ValueError(f"views of {lens} tokens, q has {n}")
         if self.n + n > self.capacity:
             raise ValueError(f"{self.n} + {n} tokens do not fit a cache of {self.capacity}")
+        if self.next_id + n > _MOST:
+            raise ValueError(f"{self.next_id} tokens were appended: {n} more have no number of 32 bits")
         at = [0]
         for x in lens:
             at.append(at[-1] + x)
@@ -300,7 +303,7 @@ class ViewCache:
         if n_keep >= self.n:
             return
         ws = self._workspace(cache_workspace_size(self.n_kv_heads, self.n, n_keep))
-        cache_evict(self.n, n_keep, self.next_id - recent, self.k, self.v, self.acc, self.ids, self._acc, self._ids, ws)
+        cache_evict(self.n, n_keep, max(self.next_id - recent, 0), self.k, self.v, self.acc, self.ids, self._acc, self._ids, ws)
         self.acc, self._acc = self._acc, self.acc
         self.ids, self._ids = self._ids, self.ids
         self.n = n_keep

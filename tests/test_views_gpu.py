@@ -879,3 +879,23 @@ def test_errors_outlive_a_workspace():
     assert e.value.status == 6
     step(3)
     c.check_device_error()  # reported once
+
+
+def test_the_last_token_numbers():
+    c = G().ViewCache(100, 2)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    step = lambda n: c.step(*(torch.randn(n, 2, 64, generator=g, device=DEV).bfloat16() for _ in range(3)))  # noqa: E731
+    c.next_id = 2 ** 31 - 51
+    step(20)
+    step(30)
+    assert c.next_id == 2 ** 31 - 1 and c.ids[:, :50].tolist() == [list(range(2 ** 31 - 51, 2 ** 31 - 1))] * 2
+    n, acc, k = c.n, c.acc.clone(), c.k.clone()
+    with pytest.raises(ValueError):
+        step(1)
+    assert c.n == n and torch.equal(c.acc, acc) and torch.equal(c.k[:n], k[:n])
+    # none of them is recent; then some; then more than there ever were
+    for keep, recent in ((40, 0), (30, 10), (20, 2 ** 40)):
+        ids, acc, last = c.ids[:, :c.n].clone(), c.acc[:, :c.n].clone(), 2 ** 31 - 1 - min(recent, 2 ** 31 - 1)
+        c.evict(keep, recent)
+        src = R.evict(acc.cpu(), ids.cpu(), keep, last).to(DEV)
+        assert torch.equal(c.ids[:, :keep], ids.gather(1, src))

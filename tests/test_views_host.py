@@ -201,3 +201,18 @@ def test_numbers_beyond_32_bits_are_refused(lib):
     with pytest.raises(ValueError, match="32 bits"):
         G.cache_workspace_size(4, 100, 2 ** 32 + 5)
     assert views._cache(4, 100, 50, 2 ** 31 - 1, 0, 0, 100).recent_from == 2 ** 31 - 1
+
+
+def test_a_cache_refuses_steps_before_it_changes(lib):
+    import sparse_global_attention_view_b200 as G
+    x = torch.zeros(6, 2, 64, dtype=torch.bfloat16)
+    c = G.ViewCache(100, 2, device="cpu")  # nothing below gets as far as a kernel
+    for lens in ([7, -1], [5], [], [6, 1]):
+        with pytest.raises(ValueError, match="views of"):
+            c.step(x, x, x, lens)
+    with pytest.raises(ValueError, match="do not fit a cache"):
+        c.step(*[torch.zeros(101, 2, 64, dtype=torch.bfloat16)] * 3)
+    c.next_id = 2 ** 31 - 6
+    with pytest.raises(ValueError, match="have no number"):
+        c.step(x, x, x)
+    assert c.n == 0 and c.next_id == 2 ** 31 - 6 and not c.ids.any()
