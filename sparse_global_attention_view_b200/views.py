@@ -268,6 +268,7 @@ class ViewCache:
                 old.record_stream(torch.cuda.current_stream(old.device))
         return self._ws
 
+    @torch.no_grad()  # copies of tensors that require gradients would tie every step's graph to the cache
     def step(self, q, k, v, lens=None, decay: float = 1.0) -> torch.Tensor:
         """Attention of the views (``lens`` tokens each; all of them one view by default) to the cache and to their
         own tokens, q [n, H, 64], k and v [n, Hk, 64]; then the tokens join the cache."""

@@ -899,3 +899,13 @@ def test_the_last_token_numbers():
         c.evict(keep, recent)
         src = R.evict(acc.cpu(), ids.cpu(), keep, last).to(DEV)
         assert torch.equal(c.ids[:, :keep], ids.gather(1, src))
+
+
+def test_a_cache_keeps_no_graph():
+    c = G().ViewCache(100, 2)
+    for _ in range(2):
+        q, k, v = (torch.randn(20, 2, 64, device=DEV).bfloat16().requires_grad_() for _ in range(3))
+        out = c.step(q, k * 1, v * 1)
+        assert not any(t.requires_grad for t in (out, c.k, c.v, c.acc))
+    c.evict(15)
+    assert c.n == 15 and not c.k.requires_grad
