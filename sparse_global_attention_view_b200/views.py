@@ -67,10 +67,13 @@ def view_workspace_size(batch: ViewBatch) -> int:
 
 
 def _new_workspace(n: int, device, stream) -> torch.Tensor:
+    if stream is not None:
+        # memory of that stream: what the current one has freed may still be in use by its kernels
+        with torch.cuda.stream(stream):
+            return _new_workspace(n, device, None)
     ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
     with torch.cuda.device(ws.device):
-        st = torch.cuda.current_stream() if stream is None else stream
-        check(load().gsa_workspace_init(ws.data_ptr(), st.cuda_stream), "gsa_workspace_init")
+        check(load().gsa_workspace_init(ws.data_ptr(), torch.cuda.current_stream().cuda_stream), "gsa_workspace_init")
     return ws
 
 

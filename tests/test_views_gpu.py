@@ -554,6 +554,24 @@ def test_another_stream():
     assert_evicted(k, v, acc, ids, 3000, 4900, *moved)
 
 
+def test_a_workspace_belongs_to_its_stream():
+    # freed memory that the current stream still writes is not handed to another stream
+    x = make(2, 2, [300], [10], 6000)
+    batch, side = batch_of(x), torch.cuda.Stream()
+    n = G().view_workspace_size(batch)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    busy = torch.empty(n, dtype=torch.uint8, device=DEV)
+    torch.cuda._sleep(50_000_000)
+    busy.fill_(255)
+    del busy
+    ws = G().new_view_workspace(batch, stream=side)
+    cache_ws = G().new_cache_workspace(2, 100, 50, stream=side)
+    torch.cuda.synchronize()
+    assert not ws[:256].any() and not cache_ws[:256].any()
+    G().check_device_error(ws, side)
+
+
 @pytest.mark.parametrize("name", list(WAYS))
 def test_captured_calls(name):
     x = make(*WAYS[name])
