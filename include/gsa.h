@@ -439,10 +439,13 @@ gsa_status prefix_attn(const gsa_view_batch* batch, const gsa_bf16* q, const gsa
  * order, as they would be appended:
  *   acc_out[hk][j] = decay * acc[hk][j] + w        (j < n_prefix),
  *   acc_out[hk][n_prefix + j] = w                  (own token j of a view).
- * acc may be NULL (an account of zeros) or acc_out itself with its stride, and
- * must not overlap it otherwise; it is not read when decay is 0.  decay is finite and >= 0.  An infinite entry stays infinite: the
- * way to have a token never evicted.  A query whose lse is -infinity counts for
- * nothing.  Slots of own tokens that belong to no view are not written.
+ * acc may be NULL (an account of zeros) or acc_out itself with its stride
+ * (any one with Hk = 1), and must not overlap it otherwise; it is not read when decay
+ * is 0.  decay is finite and >= 0.  An infinite entry stays infinite while decay is
+ * not 0: the way to have a token never evicted.  A query whose lse is -infinity counts
+ * for nothing, whatever it holds; one that holds NaN, or has an lse of NaN, makes NaN
+ * of the accounts of the keys that it sees.  Slots of own tokens that belong to no view
+ * are not written.
  * Sums are added in a fixed order: equal calls give equal bits.
  * Hk * (ceil(n_prefix / 512) + B * ceil(max_own / 512)) is at most 2^31 - 1025.
  */

@@ -177,8 +177,9 @@ gsa_status key_weights(const gsa_view_batch* batch, const gsa_bf16* q, const gsa
   if (acc_out_stride < keys || acc_out_stride >= (1LL << 40) || !(decay >= 0.f) || isinf(decay))
     return GSA_ERR_INVALID_ARG;
   if (acc != nullptr && (acc_stride < d.n_prefix || acc_stride >= (1LL << 40))) return GSA_ERR_INVALID_ARG;
-  // in place, or apart: a shifted account would be read after it was written
-  if (acc != nullptr && !(acc == acc_out && acc_stride == acc_out_stride) &&
+  // in place, or apart: a shifted account would be read after it was written.  One row
+  // has no stride
+  if (acc != nullptr && !(acc == acc_out && (acc_stride == acc_out_stride || d.Hk == 1)) &&
       overlap(acc, span(d.Hk, d.n_prefix, acc_stride), acc_out, span(d.Hk, keys, acc_out_stride)))
     return GSA_ERR_INVALID_ARG;
   const gsa::WeightsPlan p = gsa::weights_plan(d);

@@ -513,6 +513,19 @@ def test_account_of_special_values():
     assert torch.allclose(weigh(x, batch_of(x), z, None, 1.0), weigh(y, batch_of(y), z2, None, 1.0), rtol=1e-6)
 
 
+@pytest.mark.parametrize("H,Hk", [(2, 1), (4, 2)])
+@pytest.mark.parametrize("ql,tl", [([1], [9]), ([300, 280], [300, 280]), ([5, 3], [100, 50])])
+def test_an_account_in_place_by_its_slice(H, Hk, ql, tl):
+    x = make(H, Hk, ql, tl, 700)
+    z = exact_lse(x)
+    acc = torch.full((Hk, 1200 + sum(tl)), 7.0, device=DEV)
+    acc[:, :700] = torch.rand(Hk, 700, device=DEV)
+    before = acc[:, :700].clone()
+    weigh(x, batch_of(x), z, acc[:, :700], 0.5, acc)
+    assert_weights(x, acc, z, before, 0.5)
+    assert (acc[:, 700 + sum(tl):] == 7).all()
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # streams, graphs, errors
 

@@ -216,3 +216,12 @@ def test_a_cache_refuses_steps_before_it_changes(lib):
     with pytest.raises(ValueError, match="have no number"):
         c.step(x, x, x)
     assert c.n == 0 and c.next_id == 2 ** 31 - 6 and not c.ids.any()
+
+
+def test_one_row_of_an_account_has_no_stride(lib):
+    # in place, as a slice of acc_out: refused for its small workspace alone
+    for kw, status in ((dict(n_kv_heads=1), 3), (dict(n_kv_heads=2), 1)):
+        b = batch(**kw)
+        assert lib.key_weights(ctypes.byref(b), *[FAKE] * 6, FAKE, 1000, FAKE, 1200, 1.0, FAKE, 255, None) == status
+    b = batch(n_kv_heads=1)
+    assert lib.key_weights(ctypes.byref(b), *[FAKE] * 6, FAKE + 4, 1000, FAKE, 1200, 1.0, FAKE, 255, None) == 1
