@@ -354,15 +354,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (skip >> (k + 1) & 1) x1 = -CUDART_INF_F;
                   x2 = f2_pack(x0, x1);
                 }
-                const uint64_t p2 = ((2 * u + w) & 7) >= 8 - kPolyOf8 ? exp2_poly2(x2) : f2_pack(exp2_mufu(x0), exp2_mufu(x1));
+                const uint64_t p2 = ((2 * u + w) & 7) >= 8 - kPolyOf8 ? exp2_poly2<true>(x2) : f2_pack(exp2_mufu(x0), exp2_mufu(x1));
                 ps[(2 * u + w) & 3] = f2_add(ps[(2 * u + w) & 3], p2);
               }
             }
           };
           // as far as there are queries (rolled loops: registers to overlap the
-          // exponentials in, and little code; 943 us at 5496 queries and 46716 keys of
-          // 16 heads against 1159 with the next load in flight; a loop of its own for
-          // tiles whose rows all count, 896 against 934 with both in one)
+          // exponentials in, and little code; with the next load in flight 1159 us at 5496
+          // queries and 46716 keys of 16 heads, where it was 943 without; a loop of its
+          // own for tiles whose rows all count: 38 us less)
           auto load = [&](int c, bool last) {
             tmem_ld32(s_addr + 32 * c, sv);
             tmem_wait_ld();

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f2_fma(f2_pack(__uint_as_float(sv[c][2 * u]), __uint_as_float(sv[c][2 * u + 1])), c2p, nmp);
             uint64_t p2;
             if ((u & 7) >= 8 - kPolyOf8) {
-              p2 = exp2_poly2(x2);
+              p2 = exp2_poly2<false>(x2);
             } else {
               float x0, x1;
               f2_unpack(x2, x0, x1);

@@ -526,6 +526,26 @@ def test_an_account_in_place_by_its_slice(H, Hk, ql, tl):
     assert (acc[:, 700 + sum(tl):] == 7).all()
 
 
+@pytest.mark.parametrize("name", list(ACCOUNTS))
+def test_log_sums_may_be_any_number(name):
+    # far below the scores: large weights, and infinity beyond fp32; far above: nothing
+    x = make(*ACCOUNTS[name])
+    batch, z0 = batch_of(x), exact_lse(x)
+    P = x["kp"].shape[0]
+    for by in (-60.0, 40.0):
+        assert_weights(x, weigh(x, batch, z0 + by, None, 1.0), z0 + by, None, 1.0)
+    for b, rows, cols in R.views(x["q_off"], x["own_off"]):
+        for i in range(rows.start, min(rows.stop, rows.start + 16)):
+            for by, inf in ((-150.0, True), (-1e30, True), (R.NEG + 0, False), (1e30, False)):
+                z = z0.clone()
+                z[i] += by
+                got = weigh(x, batch, z, None, 1.0)
+                want = torch.zeros_like(got, dtype=torch.bool)
+                want[:, :P] = inf
+                want[:, P + cols.start:P + cols.stop] = inf
+                assert torch.equal(got == float("inf"), want) and not got.isnan().any(), (b, i, by)
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # streams, graphs, errors
 
