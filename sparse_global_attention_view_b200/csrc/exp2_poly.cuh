@@ -32,7 +32,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 
 // 2^x on the FMA pipe: x = j + f with j = round(x) and f in [-1/2, 1/2];
 // 2^f by a quartic fitted for the least maximum relative error (2.7e-6 evaluated in
-// fp32, below the 2^-9 of the bf16 weights and the 1e-5 wanted of fp32 sums of
+// fp32, below the 2^-8 of the bf16 weights and the 1e-5 wanted of fp32 sums of
 // weights), times 2^j.  x + 1.5 * 2^23 + 127 has j + 127, the exponent of 2^j, in its
 // low bits.  x is clamped at -127, where 2^j is 0: what lies below gives 0, -infinity
 // included, as the special-function unit does.  The clamp and the product keep a NaN;

@@ -34,7 +34,7 @@
 // merge_kernel: partial results only.
 //
 // Every sum, maximum and partial result is fp32; P is rounded to bf16 for the
-// product with V (a relative 2^-9 each, independent between keys), and the
+// product with V (a relative 2^-8 each at most, independent between keys), and the
 // denominator sums the unrounded weights.
 #include <cooperative_groups.h>
 #include <math.h>
